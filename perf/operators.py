@@ -1,0 +1,391 @@
+"""The 4-bit floating-point operators as measured cases.
+
+MXFP4 (blocks of 32 E2M1 values under one power-of-two E8M0 scale) and NVFP4
+(blocks of 16 under one E4M3 scale, with one float32 scale per tensor): the
+quantiser, its inverse, the product of two quantised matrices, the product of
+a few full-precision tokens with quantised weights, and the product grouped by
+expert.  Every quantised matrix is rows x n along n: codes two per byte (the
+even element in the low half), scales one byte per block, both rows padded
+with zeros to a multiple of 16 bytes.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+own = False
+
+MX, NV = 0, 1
+BLOCK = {MX: 32, NV: 16}
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+SIZE = {"bf16": 2, "f32": 4}
+DEV = "cuda"
+
+
+def listed():
+    return [
+        # A projection's rotated float32 weights become NVFP4, their dequantised values kept for the loss
+        {"name": "quantize_weight_nv", "op": "quantize", "fmt": NV, "rows": 11008, "n": 4096, "dt": "f32", "given": False},
+        # A chunk of 16384 calibration tokens, fake-quantised to MXFP4
+        {"name": "quantize_tokens_mx", "op": "quantize", "fmt": MX, "rows": 16384, "n": 8192, "dt": "bf16", "given": False},
+        # The few tokens of a decode step under a calibrated tensor scale; a ragged row
+        {"name": "quantize_step_nv", "op": "quantize", "fmt": NV, "rows": 7, "n": 4100, "dt": "bf16", "given": True},
+        # An MLP's weights back to bf16 for a library product
+        {"name": "dequantize_mlp_nv", "op": "dequantize", "fmt": NV, "rows": 28672, "n": 8192, "dt": "bf16"},
+        # A small layer with an odd row length back to float32
+        {"name": "dequantize_odd_mx", "op": "dequantize", "fmt": MX, "rows": 1000, "n": 4095, "dt": "f32"},
+        # Prefill of 2048 tokens through a gate projection
+        {"name": "matmul_prefill_nv", "op": "matmul", "fmt": NV, "T": 2048, "m": 28672, "n": 8192, "dt": "bf16"},
+        # A calibration batch through a down projection
+        {"name": "matmul_down_mx", "op": "matmul", "fmt": MX, "T": 8192, "m": 8192, "n": 28672, "dt": "bf16"},
+        # A short ragged prompt through an uneven layer, float32 results
+        {"name": "matmul_ragged_nv", "op": "matmul", "fmt": NV, "T": 100, "m": 1000, "n": 4095, "dt": "f32"},
+        # One decoded token through a q projection
+        {"name": "matvec_token_nv", "op": "matvec", "fmt": NV, "T": 1, "m": 4096, "n": 4096, "xdt": "bf16", "dt": "bf16"},
+        # Five sequences' next tokens through a down projection, float32 activations
+        {"name": "matvec_batch_mx", "op": "matvec", "fmt": MX, "T": 5, "m": 8192, "n": 28672, "xdt": "f32", "dt": "f32"},
+        # 4096 routed tokens over eight experts of unequal load
+        {"name": "grouped_prefill_nv", "op": "grouped", "fmt": NV, "E": 8, "T": 4096, "pad": 0, "m": 14336, "n": 4096, "skew": 0.5, "dt": "bf16"},
+        # A decode batch over many small experts, some without a token; spare rows at the end
+        {"name": "grouped_decode_mx", "op": "grouped", "fmt": MX, "E": 64, "T": 96, "pad": 5, "m": 2048, "n": 2048, "skew": 1.2, "dt": "bf16"},
+    ]
+
+
+def _spread(rng, lo, hi):
+    """A whole number between lo and hi, even over its logarithm."""
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["quantize", "dequantize", "matmul", "matvec", "grouped"])
+    fmt = rng.choice([MX, NV])
+    dt = rng.choice(["bf16", "f32"])
+    if op in ("quantize", "dequantize"):
+        n = _spread(rng, 16, 28672)
+        rows = _spread(rng, 1, min(16384, (1 << 27) // n))
+        case = {"op": op, "fmt": fmt, "rows": rows, "n": n, "dt": dt}
+        if op == "quantize":
+            case["given"] = fmt == NV and rng.random() < 0.5
+        return case
+    n = _spread(rng, 64, 28672)
+    if op == "matmul":
+        m = _spread(rng, 64, min(28672, (1 << 27) // n))
+        return {"op": op, "fmt": fmt, "T": _spread(rng, 1, 4096), "m": m, "n": n, "dt": dt}
+    if op == "matvec":
+        m = _spread(rng, 64, min(28672, (1 << 27) // n))
+        return {"op": op, "fmt": fmt, "T": rng.randint(1, 16), "m": m, "n": n, "xdt": rng.choice(["bf16", "f32"]), "dt": dt}
+    n = _spread(rng, 64, 8192)
+    E = _spread(rng, 1, 128)
+    m = _spread(rng, 64, max(128, min(14336, (1 << 28) // (n * E))))
+    return {"op": op, "fmt": fmt, "E": E, "T": _spread(rng, 1, 4096), "pad": rng.randint(0, 40), "m": m, "n": n,
+            "skew": round(rng.uniform(0.0, 1.5), 2), "dt": dt}
+
+
+# ------------------------------------------------------------ layout and plain forms
+def _up(v, a):
+    return -(-v // a) * a
+
+
+def _code_bytes(n):
+    return _up(-(-n // 2), 16)
+
+
+def _scale_bytes(fmt, n):
+    return _up(-(-n // BLOCK[fmt]), 16)
+
+
+def _pad_cols(x, width):
+    return torch.nn.functional.pad(x, (0, width - x.shape[1]))
+
+
+def _tensor_scale(x):
+    """max |x| over the finite values / (448 * 6), rounded to float32; 1 for a tensor of zeros."""
+    a = torch.where(torch.isfinite(x), x.abs(), 0.0).amax().double()
+    g = (a / 2688.0).float().clamp_min(2.0 ** -126)
+    return torch.where(a > 0, g, torch.ones_like(g)).reshape(1)
+
+
+def _round_e4m3(t):
+    """float64 values >= 0 to the nearest E4M3 value, ties to even, at most 448."""
+    t = t.clamp_max(448.0)
+    exponent = (torch.frexp(t).exponent - 1).clamp_min(-6)
+    step = torch.ldexp(torch.ones_like(t), exponent - 3)
+    return torch.where(t > 0, torch.round(t / step) * step, 0.0)
+
+
+def _round_e2m1(y):
+    """float64 magnitudes to indices of E2M1, ties to the even index, at most 6."""
+    return ((y > 0.25).to(torch.uint8) + (y >= 0.75) + (y > 1.25) + (y >= 1.75) + (y > 2.5) + (y >= 3.5) + (y > 5.0))
+
+
+def _plain_quantize(x, fmt, g=None):
+    """(codes 0..15 rows x n, scale bytes rows x blocks, tensor scale or None); 64 bits decide every rounding."""
+    rows, n = x.shape
+    bs = BLOCK[fmt]
+    b = _pad_cols(x, _up(n, bs)).double().reshape(rows, -1, bs)
+    amax = b.abs().amax(dim=2)
+    if fmt == MX:
+        e = torch.where(amax > 0, torch.frexp(amax).exponent - 3, -127).clamp(-127, 127)
+        scale = torch.ldexp(torch.ones_like(amax), e)
+        sbytes = (e + 127).to(torch.uint8)
+    else:
+        g = _tensor_scale(x) if g is None else g
+        s = _round_e4m3(amax / (6.0 * g.double()))
+        scale = s * g.double()
+        sbytes = s.float().to(torch.float8_e4m3fn).view(torch.uint8)
+    y = torch.where(scale[:, :, None] > 0, b.abs() / scale[:, :, None], 0.0)
+    codes = _round_e2m1(y) + 8 * torch.signbit(b)
+    return codes.reshape(rows, -1)[:, :n], sbytes, g
+
+
+def _stored(codes, sbytes, fmt):
+    """Codes two per byte and scales, rows padded with zeros."""
+    n = codes.shape[1]
+    c = _pad_cols(codes, 2 * _code_bytes(n))
+    return (c[:, 0::2] | (c[:, 1::2] << 4)).contiguous(), _pad_cols(sbytes, _scale_bytes(fmt, n)).contiguous()
+
+
+def _values(codes, sbytes, fmt, n, dtype):
+    """The values codes * scales stand for, without the tensor scale, in the given float type (exact in float32)."""
+    lut = torch.tensor(E2M1 + tuple(-v for v in E2M1), dtype=dtype, device=codes.device)
+    q = torch.stack((codes & 15, codes >> 4), dim=2).reshape(codes.shape[0], -1)
+    if fmt == MX:
+        s = torch.ldexp(torch.ones_like(sbytes, dtype=dtype), sbytes.int() - 127)
+    else:
+        s = sbytes.view(torch.float8_e4m3fn).to(dtype)
+    bs = BLOCK[fmt]
+    s = s[:, : -(-n // bs)]
+    q = q[:, : _up(n, 2)]
+    v = _pad_cols(lut[q.int()], s.shape[1] * bs).reshape(q.shape[0], -1, bs) * s[:, :, None]
+    return v.reshape(q.shape[0], -1)[:, :n]
+
+
+# ------------------------------------------------------------ states
+def _activations(gen, T, n, dt):
+    """Token rows: normal values under a few loud channels, as after a norm layer."""
+    x = torch.randn(T, n, generator=gen, device=DEV)
+    loud = torch.exp(0.5 * torch.randn(n, generator=gen, device=DEV))
+    return (x * loud).to(DTYPES[dt])
+
+
+def _weights(gen, m, n):
+    return 0.02 * torch.randn(m, n, generator=gen, device=DEV)
+
+
+def _quantized(x, fmt):
+    codes, sbytes, g = _plain_quantize(x, fmt)
+    c, s = _stored(codes, sbytes, fmt)
+    return {"c": c, "s": s, "g": g}
+
+
+def _loads(case):
+    """Tokens of each expert, heaviest first: a power law of the given steepness."""
+    w = [(e + 1.0) ** -case["skew"] for e in range(case["E"])]
+    total = sum(w)
+    sizes = [int(case["T"] * v / total) for v in w]
+    sizes[0] += case["T"] - sum(sizes)
+    return sizes
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    op, fmt = case["op"], case["fmt"]
+    st = {"case": case}
+    if op in ("quantize", "dequantize"):
+        rows, n, dt = case["rows"], case["n"], case["dt"]
+        x = _weights(gen, rows, n) if dt == "f32" else _activations(gen, rows, n, dt)
+        if op == "dequantize":
+            return st | _quantized(x, fmt) | {"out": torch.empty(rows, n, dtype=DTYPES[dt], device=DEV)}
+        st["x"] = x
+        # a calibrated scale: that of other tokens, so that some blocks saturate
+        st["g"] = 0.9 * _tensor_scale(x) if case["given"] else None
+        st["c"] = torch.empty(rows, _code_bytes(n), dtype=torch.uint8, device=DEV)
+        st["s"] = torch.empty(rows, _scale_bytes(fmt, n), dtype=torch.uint8, device=DEV)
+        st["gout"] = torch.empty(1, device=DEV) if fmt == NV else None
+        st["deq"] = torch.empty(rows, n, dtype=DTYPES[dt], device=DEV)
+        return st
+    m, n = case["m"], case["n"]
+    if op == "grouped":
+        E, T = case["E"], case["T"]
+        w = [_quantized(_weights(gen, m, n), fmt) for _ in range(E)]
+        st["w"] = {"c": torch.stack([v["c"] for v in w]), "s": torch.stack([v["s"] for v in w]),
+                   "g": torch.cat([v["g"] for v in w]) if fmt == NV else None}
+        sizes = _loads(case)
+        order = torch.randperm(E, generator=gen, device=DEV).tolist()
+        bounds = [0]
+        for e in order:
+            bounds.append(bounds[-1] + sizes[e])
+        st["bounds"] = bounds
+        st["offsets"] = torch.tensor(bounds, dtype=torch.int32, device=DEV)
+        st["x"] = _quantized(_activations(gen, T + case["pad"], n, "bf16"), fmt)
+        st["y"] = torch.zeros(T + case["pad"], m, dtype=DTYPES[case["dt"]], device=DEV)
+        return st
+    T = case["T"]
+    st["w"] = _quantized(_weights(gen, m, n), fmt)
+    if op == "matmul":
+        st["x"] = _quantized(_activations(gen, T, n, "bf16"), fmt)
+    else:
+        st["x"] = _activations(gen, T, n, case["xdt"])
+    st["y"] = torch.empty(T, m, dtype=DTYPES[case["dt"]], device=DEV)
+    return st
+
+
+def _scaled(y, x, w):
+    return y if x is None and w is None else y * (1.0 if x is None else x) * (1.0 if w is None else w)
+
+
+def _workspace_bytes(kq, case):
+    if case["op"] == "quantize":
+        return kq.kronq_fp4_quantize_workspace_bytes(case["rows"], case["n"], case["fmt"])
+    if case["op"] == "matmul":
+        return kq.kronq_fp4_matmul_workspace_bytes(case["T"], case["m"], case["n"], case["fmt"])
+    if case["op"] == "matvec":
+        return kq.kronq_fp4_matvec_workspace_bytes(case["T"], case["m"], case["n"], case["fmt"])
+    return 0
+
+
+def _run_own(st):
+    import post_quantization_kronq_b200 as kq
+
+    case = st["case"]
+    op, fmt = case["op"], case["fmt"]
+    if "ws" not in st:  # kept beside the state, as a layer keeps its own
+        st["ws"] = kq.workspace(_workspace_bytes(kq, case), DEV)
+    if op == "quantize":
+        g = st["g"] if case["given"] else st["gout"]
+        kq.kronq_fp4_quantize(st["x"], fmt, st["c"], st["s"], gscale=g, gscale_given=case["given"], deq=st["deq"], ws=st["ws"])
+        return {"values": st["deq"], "tensor_scale": None if case["given"] else g}
+    if op == "dequantize":
+        kq.kronq_fp4_dequantize(st["c"], st["s"], fmt, st["out"], gscale=st["g"])
+        return st["out"]
+    x, w = st["x"], st["w"]
+    if op == "matmul":
+        kq.kronq_fp4_matmul(x["c"], x["s"], w["c"], w["s"], fmt, case["n"], st["y"], xg=x["g"], wg=w["g"], ws=st["ws"])
+    elif op == "matvec":
+        kq.kronq_fp4_matvec(x, w["c"], w["s"], fmt, st["y"], wg=w["g"], ws=st["ws"])
+    else:
+        kq.kronq_fp4_grouped_matmul(x["c"], x["s"], st["offsets"], w["c"], w["s"], fmt, case["n"], st["y"], xg=x["g"], wg=w["g"])
+    return st["y"]
+
+
+def run(st):
+    if own:
+        return _run_own(st)
+    case = st["case"]
+    op, fmt = case["op"], case["fmt"]
+    if op == "quantize":
+        codes, sbytes, g = _plain_quantize(st["x"], fmt, st["g"])
+        c, s = _stored(codes, sbytes, fmt)
+        v = _values(c, s, fmt, case["n"], torch.float32)
+        return {"values": _scaled(v, g, None).to(DTYPES[case["dt"]]), "tensor_scale": None if case["given"] else g}
+    if op == "dequantize":
+        return _scaled(_values(st["c"], st["s"], fmt, case["n"], torch.float32), st["g"], None).to(DTYPES[case["dt"]])
+    n, dtype = case["n"], DTYPES[case["dt"]]
+    x, w = st["x"], st["w"]
+    if op == "matvec":
+        return _scaled(x.float() @ _values(w["c"], w["s"], fmt, n, torch.float32).T, None, w["g"]).to(dtype)
+    xv = _values(x["c"], x["s"], fmt, n, torch.float32)
+    if op == "matmul":
+        return _scaled(xv @ _values(w["c"], w["s"], fmt, n, torch.float32).T, x["g"], w["g"]).to(dtype)
+    y = torch.zeros(xv.shape[0], case["m"], device=DEV)
+    for e, (a, b) in enumerate(zip(st["bounds"], st["bounds"][1:])):
+        if a < b:
+            wv = _values(w["c"][e], w["s"][e], fmt, n, torch.float32)
+            y[a:b] = _scaled(xv[a:b] @ wv.T, x["g"], None if w["g"] is None else w["g"][e])
+    return y.to(dtype)
+
+
+def work(case):
+    fmt = case["fmt"]
+    per = 0.5 + 1.0 / BLOCK[fmt]  # bytes of one quantised value
+    if case["op"] == "quantize":
+        count = case["rows"] * case["n"]
+        return {"bytes": count * (2 * SIZE[case["dt"]] + per), "flops": 2 * count}
+    if case["op"] == "dequantize":
+        count = case["rows"] * case["n"]
+        return {"bytes": count * (SIZE[case["dt"]] + per), "flops": count}
+    T, m, n = case["T"], case["m"], case["n"]
+    out = T * m * SIZE[case["dt"]]
+    if case["op"] == "matvec":
+        return {"bytes": T * n * SIZE[case["xdt"]] + m * n * per + out, "flops": 2 * T * m * n}
+    used = sum(s > 0 for s in _loads(case)) if case["op"] == "grouped" else 1
+    return {"bytes": T * n * per + used * m * n * per + out, "flops": 2 * T * m * n}
+
+
+# ------------------------------------------------------------ from the definition, in 64 bits
+def _exact_values(codes, sbytes, fmt, n):
+    """Values from the bits of the formats: sign, exponent and mantissa fields."""
+    q = torch.empty(codes.shape[0], 2 * codes.shape[1], dtype=torch.int64, device=codes.device)
+    q[:, 0::2] = codes.long() & 15
+    q[:, 1::2] = codes.long() >> 4
+    q = q[:, :n]
+    e, mant = (q >> 1) & 3, (q & 1).double()
+    mag = torch.where(e == 0, 0.5 * mant, (1.0 + 0.5 * mant) * torch.exp2((e - 1).double()))
+    mag = torch.where(q >= 8, -mag, mag)
+    b = sbytes.long()
+    if fmt == MX:
+        s = torch.exp2((b - 127).double())
+    else:
+        e, mant = b >> 3, (b & 7).double()
+        s = torch.where(e == 0, mant * 2.0 ** -9, (1.0 + mant / 8.0) * torch.exp2((e - 7).double()))
+    return mag * s.repeat_interleave(BLOCK[fmt], dim=1)[:, :n]
+
+
+def _exact_fake(x, fmt, g):
+    """Nearest representable value of every element, found among all of them."""
+    rows, n = x.shape
+    bs = BLOCK[fmt]
+    wide = torch.zeros(rows, _up(n, bs), dtype=torch.float64, device=x.device)
+    wide[:, :n] = x.double()
+    b = wide.view(rows, -1, bs)
+    top = b.abs().max(dim=2).values
+    if fmt == MX:
+        e = (top.float().view(torch.int32) >> 23) - 127  # the exponent field: floor(log2) of a normal number
+        s = torch.ldexp(torch.ones_like(top), (e - 2).clamp(-127, 127))
+    else:
+        bits = torch.arange(127, device=x.device)
+        e, mant = bits >> 3, (bits & 7).double()
+        table = torch.where(e == 0, mant * 2.0 ** -9, (1.0 + mant / 8.0) * torch.exp2((e - 7).double()))
+        t = (top / (6.0 * g.double())).clamp_max(448.0)
+        hi = torch.searchsorted(table, t).clamp(1, 126)
+        below, above = t - table[hi - 1], table[hi] - t
+        take = (above < below) | ((above == below) & (hi % 2 == 0))
+        s = table[torch.where(take, hi, hi - 1)] * g.double()
+    s = s[:, :, None]
+    y = torch.where(s > 0, b.abs() / s, 0.0)
+    best, gap = torch.zeros_like(y), y.clone()
+    for i in range(1, 8):
+        d = (y - E2M1[i]).abs()
+        better = (d < gap) | ((d == gap) & (i % 2 == 0))
+        best = torch.where(better, E2M1[i], best)
+        gap = torch.minimum(gap, d)
+    return (torch.copysign(best, b) * s).view(rows, -1)[:, :n]
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    op, fmt = case["op"], case["fmt"]
+    if op == "quantize":
+        x, g = st["x"], st["g"]
+        if fmt == NV and g is None:
+            top = x.double().abs().max()
+            g = (top / (448 * 6)).float().reshape(1)
+        return {"values": _exact_fake(x, fmt, g), "tensor_scale": None if case["given"] or fmt == MX else g.double()}
+    one = torch.ones(1, dtype=torch.float64, device=DEV)
+    if op == "dequantize":
+        return _exact_values(st["c"], st["s"], fmt, case["n"]) * (one if st["g"] is None else st["g"].double())
+    n, x, w = case["n"], st["x"], st["w"]
+    wg = one if w["g"] is None else w["g"].double()
+    if op == "matvec":
+        return x.double() @ _exact_values(w["c"], w["s"], fmt, n).T * wg
+    xv = _exact_values(x["c"], x["s"], fmt, n) * (one if x["g"] is None else x["g"].double())
+    if op == "matmul":
+        return xv @ _exact_values(w["c"], w["s"], fmt, n).T * wg
+    y = torch.zeros(xv.shape[0], case["m"], dtype=torch.float64, device=DEV)
+    for e in range(case["E"]):
+        a, b = st["bounds"][e], st["bounds"][e + 1]
+        if b > a:
+            y[a:b] = xv[a:b] @ _exact_values(w["c"][e], w["s"][e], fmt, n).T * (wg[e] if fmt == NV else 1.0)
+    return y
