@@ -432,6 +432,102 @@ kronq_status kronq_decode_matvec(const uint32_t* packed, const float* scales, co
                                  const void* x, kronq_dtype xdt, float* y, void* workspace,
                                  size_t ws_bytes, kronq_stream_t s);
 
+/* ---------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (no counterpart on the pages; the same
+ * weights and tokens as the integer grids above, in the two block formats
+ * that the tensor cores multiply directly).
+ *
+ * A quantised matrix is rows x n with blocks along n, in two byte arrays:
+ *   codes   rows x kronq_fp4_code_row_bytes(n): E2M1 values (sign bit, then
+ *           0, 0.5, 1, 1.5, 2, 3, 4, 6), two per byte, the even element in
+ *           the low half;
+ *   scales  rows x kronq_fp4_scale_row_bytes(fmt, n): one byte per block, a
+ *           ragged last block included.
+ * Both row lengths are rounded up to a multiple of 16 bytes; both arrays are
+ * 16-byte aligned.  The half byte after an odd n must be 0 (kronq_fp4_quantize
+ * writes all padding as 0; the other padding is never read as data).
+ *   KRONQ_MXFP4  blocks of 32, E8M0 scales 2^(byte - 127), 255 = NaN:
+ *                value = code * scale; no tensor scale (gscale arguments NULL).
+ *   KRONQ_NVFP4  blocks of 16, E4M3 scales (unsigned), and one positive
+ *                float32 tensor scale in device memory:
+ *                value = code * scale * gscale.
+ * ------------------------------------------------------------------------- */
+typedef enum { KRONQ_MXFP4 = 0, KRONQ_NVFP4 = 1 } kronq_fp4_format;
+
+#define KRONQ_FP4_MATVEC_MAX_TOKENS 16
+#define KRONQ_FP4_MAX_EXPERTS 1024
+
+/* Bytes of a row of codes and of scales (0 for n < 1 or a bad format). */
+int64_t kronq_fp4_code_row_bytes(int64_t n);
+int64_t kronq_fp4_scale_row_bytes(kronq_fp4_format fmt, int64_t n);
+
+/* kronq_fp4_quantize -- round x (rows x n, dtype dt, row stride ldx elements)
+ * to nearest, ties to even, every decision that of exact arithmetic:
+ *   MXFP4  scale = 2^E, E = floor(log2 amax) - 2 clamped to [-127, 127]
+ *          (amax the block's largest magnitude; -127 for a block of zeros),
+ *          code = RN_e2m1(x / 2^E) saturating at 6;
+ *   NVFP4  scale = RN_e4m3(amax / (6 gscale)) saturating at 448, code =
+ *          RN_e2m1(x / (scale gscale)) saturating at 6; magnitude 0 where the
+ *          scale is 0.
+ *   gscale  NVFP4: one float (device).  gscale_given != 0: read; it must be
+ *           positive, normal and finite, otherwise every scale is NaN.
+ *           gscale_given == 0: computed and written,
+ *           max(RN_f32(A / 2688), 2^-126) with A the largest finite magnitude
+ *           of x, or 1 when A is 0 (448 * 6 = 2688).
+ *   A block that holds a NaN or an infinity gets the format's NaN scale and
+ *   codes 0; the other blocks are not affected by it.
+ *   deq     NULL, or rows x n values of dtype dt (row stride ldd): the values
+ *           that codes and scales stand for (code * scale * gscale in float32,
+ *           rounded to dt).  May be x itself (with ldd == ldx).
+ *   workspace  kronq_fp4_quantize_workspace_bytes(rows, n, fmt), 256-byte
+ *           aligned; needed only where the tensor scale is computed.
+ * rows may be 0.  Asynchronous on s. */
+size_t kronq_fp4_quantize_workspace_bytes(int64_t rows, int64_t n, kronq_fp4_format fmt);
+kronq_status kronq_fp4_quantize(const void* x, kronq_dtype dt, int64_t rows, int64_t n, int64_t ldx,
+                                kronq_fp4_format fmt, uint8_t* codes, uint8_t* scales, float* gscale,
+                                int gscale_given, void* deq, int64_t ldd, void* workspace, size_t ws_bytes,
+                                kronq_stream_t s);
+
+/* kronq_fp4_dequantize -- out (rows x n, dtype dt, row stride ldo) = code *
+ * scale * gscale, computed in float32 and rounded to dt. */
+kronq_status kronq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, const float* gscale,
+                                  kronq_fp4_format fmt, int64_t rows, int64_t n, void* out, kronq_dtype dt,
+                                  int64_t ldo, kronq_stream_t s);
+
+/* kronq_fp4_matmul -- y = X W^T for tokens X (T x n) and weights W (m x n),
+ * both quantised in the same format: y (T x m, dtype ydt, row stride ldy),
+ * products exact, sums in float32, the tensor scales applied to the sums.
+ * workspace: kronq_fp4_matmul_workspace_bytes(T, m, n, fmt) bytes (0 where n
+ * is not split), 256-byte aligned.  T may be 0.  y may not overlap an input.
+ * Asynchronous on s. */
+size_t kronq_fp4_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n, kronq_fp4_format fmt);
+kronq_status kronq_fp4_matmul(const uint8_t* xc, const uint8_t* xs, const float* xg, const uint8_t* wc,
+                              const uint8_t* ws, const float* wg, kronq_fp4_format fmt, int64_t T, int64_t m,
+                              int64_t n, void* y, kronq_dtype ydt, int64_t ldy, void* workspace, size_t ws_bytes,
+                              kronq_stream_t s);
+
+/* kronq_fp4_matvec -- y = X W^T for at most KRONQ_FP4_MATVEC_MAX_TOKENS
+ * tokens X (T x n, bf16 or float32, row stride ldx) that are not quantised
+ * (single-token decode with 4-bit weights); products and sums in float32.
+ * Other arguments as kronq_fp4_matmul. */
+size_t kronq_fp4_matvec_workspace_bytes(int64_t T, int64_t m, int64_t n, kronq_fp4_format fmt);
+kronq_status kronq_fp4_matvec(const void* x, kronq_dtype xdt, int64_t ldx, const uint8_t* wc, const uint8_t* ws,
+                              const float* wg, kronq_fp4_format fmt, int64_t T, int64_t m, int64_t n, void* y,
+                              kronq_dtype ydt, int64_t ldy, void* workspace, size_t ws_bytes, kronq_stream_t s);
+
+/* kronq_fp4_grouped_matmul -- tokens grouped by expert: rows
+ * [offsets[e], offsets[e + 1]) of X are multiplied by expert e's weights.
+ *   offsets  E + 1 ints (device), not decreasing, within [0, T]; a group may
+ *            be empty.  Offsets outside that range are taken as the nearest
+ *            valid ones (each at least its predecessor, at most T).
+ *   wc, ws   E x m rows as one array; wg E floats (NVFP4), xg one.
+ *   Rows of y that belong to no group are left as they were.
+ * E in 1 .. KRONQ_FP4_MAX_EXPERTS.  Asynchronous on s, no workspace. */
+kronq_status kronq_fp4_grouped_matmul(const uint8_t* xc, const uint8_t* xs, const float* xg, const int* offsets,
+                                      int64_t E, const uint8_t* wc, const uint8_t* ws, const float* wg,
+                                      kronq_fp4_format fmt, int64_t T, int64_t m, int64_t n, void* y,
+                                      kronq_dtype ydt, int64_t ldy, kronq_stream_t s);
+
 /* Number of kernels this library has launched in the process so far (all
  * devices and streams); a host counter, no synchronisation. */
 uint64_t kronq_launch_count(void);

@@ -10,8 +10,8 @@ from __future__ import annotations
 
 import ctypes
 
-from ._lib import (BF16, BIIP_MODES, F32, ORDERED_FP32, R_FORM, U_GIVEN, WRITE_E, KronqError,
-                   QuantParams, check, lib)
+from ._lib import (BF16, BIIP_MODES, F32, MXFP4, NVFP4, ORDERED_FP32, R_FORM, U_GIVEN, WRITE_E,
+                   KronqError, QuantParams, check, lib)
 
 __all__ = [
     "KronqError", "QuantParams", "U_GIVEN", "ORDERED_FP32", "WRITE_E", "R_FORM",
@@ -27,6 +27,10 @@ __all__ = [
     "EST_INPUT", "EST_MARGINAL", "EST_FROBENIUS", "EST_FLIPFLOP",
     "kronq_kron_factors_workspace_bytes", "kronq_kron_factors",
     "kronq_decode_matvec_workspace_bytes", "kronq_decode_matvec",
+    "MXFP4", "NVFP4", "kronq_fp4_code_row_bytes", "kronq_fp4_scale_row_bytes",
+    "kronq_fp4_quantize_workspace_bytes", "kronq_fp4_quantize", "kronq_fp4_dequantize",
+    "kronq_fp4_matmul_workspace_bytes", "kronq_fp4_matmul", "kronq_fp4_matvec_workspace_bytes",
+    "kronq_fp4_matvec", "kronq_fp4_grouped_matmul",
 ]
 
 # kronq_estimator (Table 1 rows of the "WaterKron and FlipFlop Hessian" page)
@@ -304,3 +308,165 @@ def kronq_kfac_loss(E, HG, ws=None, stream=None) -> float:
     check(lib.kronq_kfac_loss(_ptr(E), _ptr(HG), m, n, ctypes.byref(out), _ptr(ws), ws.numel(),
                               _stream(stream)))
     return out.value
+
+
+# ------------------------------------------------------------ microscaled 4-bit floating point
+def kronq_fp4_code_row_bytes(n: int) -> int:
+    return int(lib.kronq_fp4_code_row_bytes(n))
+
+
+def kronq_fp4_scale_row_bytes(fmt: int, n: int) -> int:
+    return int(lib.kronq_fp4_scale_row_bytes(fmt, n))
+
+
+def _fp4_call(fn, device, stream, *args):
+    """One library call with the tensors' device current, on the given stream or that device's current one."""
+    import torch
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            check(fn(*args, _stream(stream)))
+    else:
+        check(fn(*args, _stream(stream)))
+
+
+def _fp4_rows(t, name):
+    """A two-dimensional device matrix whose rows are dense (any row stride)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with unit stride along its rows")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live in device memory")
+    return t
+
+
+def _fp4_ld(t):
+    """Row stride in elements (a single row may carry any stride)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _fp4_bytes(t, name, shape, device):
+    import torch
+    if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous uint8 of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must live on {device}")
+
+
+def _fp4_scale(t, name, fmt, count, device):
+    import torch
+    if (t is None) == (fmt == NVFP4):
+        raise ValueError(f"{name}: a float32 tensor scale goes with NVFP4 and with it only")
+    if t is not None and (t.dtype != torch.float32 or t.numel() != count or t.device != device
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must hold {count} float32 on {device}")
+
+
+def _fp4_ws(ws, need, device):
+    if ws is None:
+        return workspace(need, device) if need else None
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {device}")
+    return ws
+
+
+def _fp4_ws_args(ws):
+    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+
+
+def kronq_fp4_quantize_workspace_bytes(rows: int, n: int, fmt: int) -> int:
+    return int(lib.kronq_fp4_quantize_workspace_bytes(rows, n, fmt))
+
+
+def kronq_fp4_quantize(x, fmt: int, codes, scales, gscale=None, gscale_given: bool = False, deq=None, ws=None,
+                       stream=None):
+    """codes, scales (and NVFP4's gscale, unless given) of x (rows x n, bf16 or
+    float32, dense rows); deq (x's type) receives the values they stand for."""
+    _fp4_rows(x, "x")
+    rows, n = x.shape
+    dev = x.device
+    _fp4_bytes(codes, "codes", (rows, kronq_fp4_code_row_bytes(n)), dev)
+    _fp4_bytes(scales, "scales", (rows, kronq_fp4_scale_row_bytes(fmt, n)), dev)
+    _fp4_scale(gscale, "gscale", fmt, 1, dev)
+    if deq is not None:
+        _fp4_rows(deq, "deq")
+        if deq.shape != x.shape or deq.dtype != x.dtype or deq.device != dev:
+            raise ValueError("deq must have x's shape, type and device")
+    if fmt == NVFP4 and not gscale_given:
+        ws = _fp4_ws(ws, kronq_fp4_quantize_workspace_bytes(rows, n, fmt), dev)
+    else:
+        ws = None
+    _fp4_call(lib.kronq_fp4_quantize, dev, stream, _ptr(x), _dtype_code(x), rows, n, _fp4_ld(x), fmt, _ptr(codes),
+              _ptr(scales), _ptr(gscale), 1 if gscale_given else 0, _ptr(deq), 0 if deq is None else _fp4_ld(deq),
+              *_fp4_ws_args(ws))
+
+
+def kronq_fp4_dequantize(codes, scales, fmt: int, out, gscale=None, stream=None):
+    """out (rows x n, bf16 or float32, dense rows) = the values of codes and scales."""
+    _fp4_rows(out, "out")
+    rows, n = out.shape
+    dev = out.device
+    _fp4_bytes(codes, "codes", (rows, kronq_fp4_code_row_bytes(n)), dev)
+    _fp4_bytes(scales, "scales", (rows, kronq_fp4_scale_row_bytes(fmt, n)), dev)
+    _fp4_scale(gscale, "gscale", fmt, 1, dev)
+    _fp4_call(lib.kronq_fp4_dequantize, dev, stream, _ptr(codes), _ptr(scales), _ptr(gscale), fmt, rows, n, _ptr(out),
+              _dtype_code(out), _fp4_ld(out))
+
+
+def kronq_fp4_matmul_workspace_bytes(T: int, m: int, n: int, fmt: int) -> int:
+    return int(lib.kronq_fp4_matmul_workspace_bytes(T, m, n, fmt))
+
+
+def kronq_fp4_matmul(xc, xs, wc, wsc, fmt: int, n: int, y, xg=None, wg=None, ws=None, stream=None):
+    """y (T x m, bf16 or float32, dense rows) = X W^T for quantised X (T x n)
+    and W (m x n), each as codes, scales and (NVFP4) a tensor scale."""
+    _fp4_rows(y, "y")
+    T, m = y.shape
+    dev = y.device
+    lc, ls = kronq_fp4_code_row_bytes(n), kronq_fp4_scale_row_bytes(fmt, n)
+    _fp4_bytes(xc, "xc", (T, lc), dev), _fp4_bytes(xs, "xs", (T, ls), dev)
+    _fp4_bytes(wc, "wc", (m, lc), dev), _fp4_bytes(wsc, "wsc", (m, ls), dev)
+    _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, 1, dev)
+    ws = _fp4_ws(ws, kronq_fp4_matmul_workspace_bytes(T, m, n, fmt) if ws is None else 0, dev)
+    _fp4_call(lib.kronq_fp4_matmul, dev, stream, _ptr(xc), _ptr(xs), _ptr(xg), _ptr(wc), _ptr(wsc), _ptr(wg), fmt, T,
+              m, n, _ptr(y), _dtype_code(y), _fp4_ld(y), *_fp4_ws_args(ws))
+
+
+def kronq_fp4_matvec_workspace_bytes(T: int, m: int, n: int, fmt: int) -> int:
+    return int(lib.kronq_fp4_matvec_workspace_bytes(T, m, n, fmt))
+
+
+def kronq_fp4_matvec(x, wc, wsc, fmt: int, y, wg=None, ws=None, stream=None):
+    """y (T x m, bf16 or float32) = X W^T for at most 16 tokens X (T x n, bf16
+    or float32, not quantised) and quantised W (m x n)."""
+    _fp4_rows(x, "x"), _fp4_rows(y, "y")
+    T, n = x.shape
+    m = y.shape[1]
+    dev = y.device
+    if y.shape[0] != T or x.device != dev:
+        raise ValueError("x and y must have the same rows and device")
+    _fp4_bytes(wc, "wc", (m, kronq_fp4_code_row_bytes(n)), dev)
+    _fp4_bytes(wsc, "wsc", (m, kronq_fp4_scale_row_bytes(fmt, n)), dev)
+    _fp4_scale(wg, "wg", fmt, 1, dev)
+    ws = _fp4_ws(ws, kronq_fp4_matvec_workspace_bytes(T, m, n, fmt) if ws is None else 0, dev)
+    _fp4_call(lib.kronq_fp4_matvec, dev, stream, _ptr(x), _dtype_code(x), _fp4_ld(x), _ptr(wc), _ptr(wsc), _ptr(wg),
+              fmt, T, m, n, _ptr(y), _dtype_code(y), _fp4_ld(y), *_fp4_ws_args(ws))
+
+
+def kronq_fp4_grouped_matmul(xc, xs, offsets, wc, wsc, fmt: int, n: int, y, xg=None, wg=None, stream=None):
+    """Rows [offsets[e], offsets[e + 1]) of y = those of X times expert e's
+    weights: wc, wsc (E x m x row bytes), wg (E float32, NVFP4), offsets
+    (E + 1 int32).  Rows of no group are left as they were."""
+    import torch
+    _fp4_rows(y, "y")
+    T, m = y.shape
+    dev = y.device
+    E = offsets.numel() - 1
+    if offsets.dtype != torch.int32 or offsets.device != dev or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be contiguous int32 on {dev}")
+    lc, ls = kronq_fp4_code_row_bytes(n), kronq_fp4_scale_row_bytes(fmt, n)
+    _fp4_bytes(xc, "xc", (T, lc), dev), _fp4_bytes(xs, "xs", (T, ls), dev)
+    _fp4_bytes(wc, "wc", (E, m, lc), dev), _fp4_bytes(wsc, "wsc", (E, m, ls), dev)
+    _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, E, dev)
+    _fp4_call(lib.kronq_fp4_grouped_matmul, dev, stream, _ptr(xc), _ptr(xs), _ptr(xg), _ptr(offsets), E, _ptr(wc),
+              _ptr(wsc), _ptr(wg), fmt, T, m, n, _ptr(y), _dtype_code(y), _fp4_ld(y))

@@ -17,6 +17,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_NOT_PD, ERR_TIMEOUT = range(
 BF16, F32 = 0, 1
 BIIP_MODES = {"full": 0, "no_rescale": 1, "su_only": 2, "sv_only": 3}
 U_GIVEN, ORDERED_FP32, WRITE_E, R_FORM = 1, 2, 4, 8
+MXFP4, NVFP4 = 0, 1
 
 STATUS_NAMES = {0: "KRONQ_OK", 1: "KRONQ_ERR_INVALID_ARG", 2: "KRONQ_ERR_UNSUPPORTED",
                 3: "KRONQ_ERR_CUDA", 4: "KRONQ_ERR_NOT_PD", 5: "KRONQ_ERR_TIMEOUT"}
@@ -76,6 +77,20 @@ SIGNATURES = {
     "kronq_decode_matvec_workspace_bytes": (_sz, [_i64, _i64]),
     "kronq_decode_matvec": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _int, _u64, _int, _vp, _vp, _vp,
                                    _int, _vp, _vp, _sz, _vp]),
+    "kronq_fp4_code_row_bytes": (_i64, [_i64]),
+    "kronq_fp4_scale_row_bytes": (_i64, [_int, _i64]),
+    "kronq_fp4_quantize_workspace_bytes": (_sz, [_i64, _i64, _int]),
+    "kronq_fp4_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _i64, _vp,
+                                  _sz, _vp]),
+    "kronq_fp4_dequantize": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _vp, _int, _i64, _vp]),
+    "kronq_fp4_matmul_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "kronq_fp4_matmul": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _vp,
+                                _sz, _vp]),
+    "kronq_fp4_matvec_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "kronq_fp4_matvec": (_int, [_vp, _int, _i64, _vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _int, _i64,
+                                _vp, _sz, _vp]),
+    "kronq_fp4_grouped_matmul": (_int, [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _int, _i64, _i64, _i64,
+                                        _vp, _int, _i64, _vp]),
     "kronq_launch_count": (ctypes.c_uint64, []),
     "kronq_last_error": (ctypes.c_char_p, []),
     "kronq_version": (ctypes.c_char_p, []),

@@ -1,0 +1,56 @@
+// The microscaled 4-bit formats' layout and device conversions, shared by the
+// quantiser, its inverse and the products.
+//
+// A quantised matrix (rows x n, blocks along n) is two byte arrays:
+//   codes   rows x code_row_bytes(n): two E2M1 codes a byte, the even element
+//           in the low half;
+//   scales  rows x scale_row_bytes(fmt, n): one byte per block of 32 (MXFP4,
+//           E8M0) or 16 (NVFP4, E4M3) elements.
+// Both row lengths are rounded up to 16 bytes (what TMA and 16-byte loads
+// need), the padding is zero.  NVFP4 has one float32 scale per tensor on top.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace kq {
+
+inline bool fp4_fmt_ok(int fmt) { return fmt == KRONQ_MXFP4 || fmt == KRONQ_NVFP4; }
+inline int fp4_block(int fmt) { return fmt == KRONQ_MXFP4 ? 32 : 16; }
+inline int64_t fp4_code_row(int64_t n) { return ceil_div(ceil_div(n, 2), 16) * 16; }
+inline int64_t fp4_scale_row(int fmt, int64_t n) { return ceil_div(ceil_div(n, fp4_block(fmt)), 16) * 16; }
+
+// Largest row and column counts of the 4-bit calls: coordinates of the
+// tensor maps and tile indices are 32-bit.
+constexpr int64_t kFp4MaxDim = int64_t(1) << 30;
+
+// Value of an E8M0 byte (255 is NaN) and of an E4M3 byte (0x7F is NaN).
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  // 2^-127 (b = 0) is a float32 subnormal
+  return b == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(b ? b << 23 : 0x00400000u);
+}
+__device__ __forceinline__ float e4m3_value(uint32_t b) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(b));
+  return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+}
+template <int FMT>
+__device__ __forceinline__ float fp4_scale_value(uint32_t b) {
+  return FMT == KRONQ_MXFP4 ? e8m0_value(b) : e4m3_value(b);
+}
+
+// Two E2M1 codes (a byte, the first in the low half) as a pair of halves.
+__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h) : "r"(byte));
+  return h;
+}
+__device__ __forceinline__ float2 e2m1x2_float2(uint32_t byte) {
+  const uint32_t h = e2m1x2_f16x2(byte);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace kq
