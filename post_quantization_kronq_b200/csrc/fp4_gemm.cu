@@ -1,0 +1,552 @@
+// Product of two microscaled 4-bit matrices on the tensor cores, plain or
+// grouped by expert: y[t, r] = gx gw sum_k X[t, k] W[r, k].
+//
+// tcgen05 multiplies E2M1 operands with their block scales (kind::mxf4nvf4
+// with four E4M3 scales per 64 columns, kind::mxf4 with two E8M0 ones) at four
+// times the bf16 rate; accumulation is float32 in TMEM, the tensor scales
+// multiply the sums.  The weights are the M side: a pair of SMs
+// (cta_group::2) owns 256 rows of W and up to 256 tokens (N, a multiple of
+// 64, so few tokens cost few columns), 128 rows and half of the tokens' codes
+// in each CTA.  Per 256-column chunk a CTA stages 128 bytes of codes of each
+// of its rows by TMA (128-byte swizzle).
+//
+// Scales: the tensor core wants, for 128 rows and 4 scale bytes, 32 lanes x 4
+// words with row r in lane r % 32, word r / 32.  The user's layout is row by
+// row, so four loader warps read 16 bytes of four rows 32 apart, transpose
+// the 4 x 4 words in registers and store 16-byte rows of four such 512-byte
+// atoms; tcgen05.cp spreads an atom over TMEM.  A loader step covers 64 bytes
+// of scales of every row (1024 or 2048 columns), double-buffered.  A tile of
+// 256 x 256 leaves 256 of the 512 TMEM columns for scales; the eight epilogue
+// warps drain the accumulator into registers first and release it before they
+// store.
+//
+// Warps: 0 TMA, 1 MMA (lane 0 of the even CTA), 2-5 scales, 6-13 epilogue.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "fp4.cuh"
+#include "fp4_gemm.h"
+#include "internal.h"
+
+namespace kq {
+namespace {
+
+constexpr int GM = 256, GH = 128, GN = 256;   // rows of W per pair, per CTA; most tokens per tile
+constexpr int NG = 64;                        // granularity of a tile's tokens
+constexpr int CK = 256;                       // columns per chunk: 128 bytes of codes
+constexpr int WBOX = GH * 128;                // 16 KB
+constexpr int XROWS = NG / 2;                 // token rows of one TMA box
+constexpr int XBOX = XROWS * 128;             // 4 KB
+constexpr int STAGES = 5;
+constexpr int STAGE = WBOX + GH * 128;        // 32 KB
+constexpr int PIECE = 3 * 2048;               // 16 scale bytes of 128 + 256 rows, as atoms
+constexpr int SFBUF = 4 * PIECE;              // one loader step
+constexpr int GROUP_INTS = 2 * (KRONQ_FP4_MAX_EXPERTS + 1);
+constexpr int THREADS = 448;
+constexpr int LOADERS = 4, EPI = 8;
+constexpr int SMEM = STAGES * STAGE + 2 * SFBUF + 256 + GROUP_INTS * 4 + 1024;
+constexpr uint32_t SF_COL = GN;               // TMEM columns of the scales: 4 chunks of 48
+
+struct GemmArgs {
+  const uint8_t *xs, *ws;
+  const float *xg, *wg;
+  const int* offsets;     // grouped: E + 1 bounds, else NULL
+  int E;
+  int64_t T, m, lds;
+  int kb;                 // scale bytes of a row that are data
+  int nchunks, tiles_m;
+  int splits, per_split;  // chunks of a split
+  void* y;
+  int64_t ldy;
+  float* part;            // split partial sums [split][T][m], or NULL
+};
+
+// Tile u of the persistent loop.
+struct Tile {
+  int e;            // expert
+  int64_t m0;       // first row within the expert
+  int64_t t0, t1;   // tokens
+  int cols;         // N: tokens rounded up to NG
+  int c0, c1;       // chunks
+  int split;
+};
+
+// Group bounds and first tiles, and the walk over tiles: up to eight token
+// tiles of a group run next to each other on the same rows of W, so that W
+// comes from L2 after its first reader.
+struct Walk {
+  const int* bound;
+  const int* first;
+  int ntiles;
+
+  __device__ __forceinline__ bool get(const GemmArgs& a, int u, Tile& t) const {
+    if (u >= ntiles) return false;
+    t.split = u % a.splits;
+    u /= a.splits;
+    int e = 0;
+    int64_t lo = 0, hi = a.T;
+    if (a.offsets) {
+      int l = 0, h = a.E - 1;   // the last group whose first tile is <= u
+      while (l < h) {
+        const int mid = (l + h + 1) >> 1;
+        if (first[mid] <= u) l = mid; else h = mid - 1;
+      }
+      e = l;
+      u -= first[e];
+      lo = bound[e];
+      hi = bound[e + 1];
+    }
+    const int tn = (int)((hi - lo + GN - 1) / GN);
+    const int band = 8 * a.tiles_m;
+    const int b = u / band, in = u - b * band;
+    const int width = min(8, tn - 8 * b);
+    const int i = in / width, j = 8 * b + (in - i * width);
+    t.e = e;
+    t.m0 = (int64_t)i * GM;
+    t.t0 = lo + (int64_t)j * GN;
+    t.t1 = min(hi, t.t0 + GN);
+    t.cols = ((int)(t.t1 - t.t0) + NG - 1) / NG * NG;
+    t.c0 = t.split * a.per_split;
+    t.c1 = min(a.nchunks, t.c0 + a.per_split);
+    return true;
+  }
+};
+
+// Bounds as documented (each at least its predecessor, within [0, T]) and the
+// number of tiles before each group, by one warp.
+__device__ void group_walk(const GemmArgs& a, int* bound, int* first, int lane) {
+  int top = 0;
+  for (int i0 = 0; i0 <= a.E; i0 += 32) {
+    const int i = i0 + lane;
+    int v = i <= a.E ? (int)min((int64_t)max(a.offsets[i], 0), a.T) : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int p = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, p);
+    }
+    v = max(v, top);
+    if (i <= a.E) bound[i] = v;
+    top = __shfl_sync(0xffffffffu, v, 31);
+  }
+  __syncwarp();
+  int sum = 0;
+  for (int i0 = 0; i0 < a.E; i0 += 32) {
+    const int i = i0 + lane;
+    const int own = i < a.E ? (bound[i + 1] - bound[i] + GN - 1) / GN * a.tiles_m : 0;
+    int v = own;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int p = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += p;
+    }
+    if (i < a.E) first[i] = sum + v - own;
+    sum += __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (lane == 0) first[a.E] = sum;
+}
+
+// Descriptor of a 512-byte scale atom: no swizzle, 8-row groups of 16-byte rows.
+__device__ __forceinline__ uint64_t atom_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
+         ((uint64_t)1 << 46);
+}
+__device__ __forceinline__ void copy_atom(uint32_t tcol, uint32_t saddr) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tcol), "l"(atom_desc(saddr)) : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+  if (FMT == KRONQ_NVFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor: E2M1 operands (both K-major), scale type E4M3 (0) or
+// E8M0 (1), M 256; id selects the first scale byte of a word (MXFP4: 0 or 2).
+template <int FMT>
+__device__ __forceinline__ uint32_t fp4_idesc(int cols, uint32_t id) {
+  return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(cols >> 3) << 17) |
+         ((FMT == KRONQ_MXFP4 ? 1u : 0u) << 23) | ((uint32_t)(GM >> 4) << 24) | (id << 29);
+}
+
+// Bytes of word j of a 16-byte piece of which `valid` bytes are data.
+__device__ __forceinline__ uint32_t tail_mask(int valid, int j) {
+  const int left = valid - 4 * j;
+  return left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+}
+
+template <int FMT, bool BF16, bool PART>
+__global__ void __launch_bounds__(THREADS, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const GemmArgs a) {
+  // chunks per 16-byte scale piece and per loader step
+  constexpr int CPP = FMT == KRONQ_NVFP4 ? 1 : 2, CPS = 4 * CPP;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sfmem = smem + STAGES * STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sfmem + 2 * SFBUF);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
+  const uint32_t sffull0 = empty0 + 8 * STAGES, sfempty0 = sffull0 + 16;
+  const uint32_t accfull = sfempty0 + 16, accempty = accfull + 8, done = accempty + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 7);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* bound = reinterpret_cast<int*>(sfmem + 2 * SFBUF + 256);
+  int* first = bound + KRONQ_FP4_MAX_EXPERTS + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cl_rank();
+  const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(sffull0 + 8 * b, 2 * LOADERS);
+      mbar_init(sfempty0 + 8 * b, 1);
+    }
+    mbar_init(accfull, 1);
+    mbar_init(accempty, 2 * EPI);
+    mbar_init(done, 1);
+    *abort_s = 0;
+    fence_mbar_init();
+    prefetch_tmap(&mW);
+    prefetch_tmap(&mX);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 2 && a.offsets) group_walk(a, bound, first, lane);
+  tc_fence_before();
+  cl_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk;
+  walk.bound = bound;
+  walk.first = first;
+  walk.ntiles = a.offsets ? first[a.E] : a.tiles_m * (int)((a.T + GN - 1) / GN) * a.splits;
+  Tile t;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t full_lead = cl_map(full0, 0);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = pair; ok && walk.get(a, u, t); u += npairs) {
+        const int rw = (int)((int64_t)t.e * a.m + t.m0) + GH * (int)rank;
+        const int boxes = t.cols / NG;
+        const int rx = (int)t.t0 + (t.cols / 2) * (int)rank;
+        for (int c = t.c0; c < t.c1; ++c, ++it) {
+          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
+          if (*abort_s || !mbar_wait(empty0 + 8 * s, ph ^ 1)) {
+            *abort_s = 1;
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2u * (uint32_t)(WBOX + boxes * XBOX));
+          const uint32_t st = smem_u32(smem) + s * STAGE, fb = full_lead + 8 * s;
+          tma_load_2d_pair(st, &mW, fb, c * (CK / 2), rw);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d_pair(st + WBOX + b * XBOX, &mX, fb, c * (CK / 2), rx + b * XROWS);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      uint32_t it = 0, sit = 0;
+      int done_tiles = 0;
+      bool ok = true, issued = false;
+      for (int u = pair; ok && walk.get(a, u, t); u += npairs, ++done_tiles) {
+        if (done_tiles > 0 && (*abort_s || !mbar_wait(accempty, (done_tiles - 1) & 1))) {
+          *abort_s = 1;
+          break;
+        }
+        tc_fence_after();
+        const int halves = (t.cols + GH - 1) / GH;
+        for (int c = t.c0; c < t.c1; ++c, ++it) {
+          const int lc = c - t.c0, in = lc % CPS;
+          if (in == 0 && (*abort_s || !mbar_wait(sffull0 + 8 * (sit & 1), (sit >> 1) & 1))) {
+            *abort_s = 1;
+            ok = false;
+            break;
+          }
+          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
+          if (*abort_s || !mbar_wait(full0 + 8 * s, ph)) {
+            *abort_s = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t piece = smem_u32(sfmem) + (sit & 1) * SFBUF + (in / CPP) * PIECE;
+          const uint32_t sf = tmem + SF_COL + (it & 3) * 48;
+#pragma unroll
+          for (int j = 0; j < 4 / CPP; ++j) {
+            const uint32_t atom = piece + (CPP == 1 ? j : 2 * (in & 1) + j) * 512;
+            copy_atom(sf + 4 * j, atom);
+            copy_atom(sf + 16 + 8 * j, atom + 2048);
+            if (halves > 1) copy_atom(sf + 20 + 8 * j, atom + 4096);
+          }
+          const uint32_t st = smem_u32(smem) + s * STAGE;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const int j = kk / CPP;
+            mma_fp4_pair<FMT>(tmem, smem_desc_sw128(st + kk * 32, 16, 1024),
+                              smem_desc_sw128(st + WBOX + kk * 32, 16, 1024),
+                              fp4_idesc<FMT>(t.cols, CPP == 1 ? 0u : 2u * (kk & 1)), sf + 4 * j, sf + 16 + 8 * j,
+                              (lc | kk) != 0 ? 1u : 0u);
+          }
+          issued = true;
+          mma_commit_pair_mc(empty0 + 8 * s, 0x3);
+          if (in == CPS - 1 || c + 1 == t.c1) {
+            mma_commit_pair_mc(sfempty0 + 8 * (sit & 1), 0x3);
+            ++sit;
+          }
+        }
+        if (ok) mma_commit_pair_mc(accfull, 0x3);
+      }
+      if (issued) {
+        mma_commit_pair_mc(done, 0x1);
+        mbar_wait(done, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 2 + LOADERS) {
+    const int i = 8 * (warp - 2) + (lane & 7), p = lane >> 3;   // row modulo 32, piece of the step
+    const uint32_t lead = cl_map(sffull0, 0);
+    uint32_t sit = 0;
+    bool ok = true;
+    const int64_t wlast = (int64_t)a.E * a.m - 1;
+    for (int u = pair; ok && walk.get(a, u, t); u += npairs) {
+      const int halves = (t.cols + GH - 1) / GH;
+      // rows beyond the matrices read its last row: their results are not stored
+      const uint8_t* row[12];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t r = (int64_t)t.e * a.m + t.m0 + GH * (int64_t)rank + i + 32 * q;
+        row[q] = a.ws + min(r, wlast) * a.lds;
+        row[4 + q] = a.xs + min(t.t0 + i + 32 * q, a.T - 1) * a.lds;
+        row[8 + q] = a.xs + min(t.t0 + GH + i + 32 * q, a.T - 1) * a.lds;
+      }
+      for (int c = t.c0; c < t.c1; c += CPS, ++sit) {
+        const int byte = 16 * (c / CPP + p);
+        const int valid = a.kb - byte;
+        uint4 v[12];
+#pragma unroll
+        for (int q = 0; q < 12; ++q)
+          v[q] = valid > 0 && (q < 8 || halves > 1) ? __ldg(reinterpret_cast<const uint4*>(row[q] + byte))
+                                                    : make_uint4(0, 0, 0, 0);
+        if (valid > 0 && valid < 16) {
+#pragma unroll
+          for (int q = 0; q < 12; ++q) {
+            v[q].x &= tail_mask(valid, 0);
+            v[q].y &= tail_mask(valid, 1);
+            v[q].z &= tail_mask(valid, 2);
+            v[q].w &= tail_mask(valid, 3);
+          }
+        }
+        int good = 1;
+        if (lane == 0) good = !*abort_s && mbar_wait(sfempty0 + 8 * (sit & 1), ((sit >> 1) & 1) ^ 1) ? 1 : 0;
+        good = __shfl_sync(0xffffffffu, good, 0);
+        if (!good) {
+          if (lane == 0) *abort_s = 1;
+          ok = false;
+          break;
+        }
+        uint8_t* dst = sfmem + (sit & 1) * SFBUF + p * PIECE + i * 16;
+#pragma unroll
+        for (int g = 0; g < 3; ++g) {
+          if (g < 1 + halves) {
+            uint4* o = reinterpret_cast<uint4*>(dst + g * 2048);
+            o[0] = make_uint4(v[4 * g].x, v[4 * g + 1].x, v[4 * g + 2].x, v[4 * g + 3].x);
+            o[32] = make_uint4(v[4 * g].y, v[4 * g + 1].y, v[4 * g + 2].y, v[4 * g + 3].y);
+            o[64] = make_uint4(v[4 * g].z, v[4 * g + 1].z, v[4 * g + 2].z, v[4 * g + 3].z);
+            o[96] = make_uint4(v[4 * g].w, v[4 * g + 1].w, v[4 * g + 2].w, v[4 * g + 3].w);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead + 8 * (sit & 1));
+      }
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2 - LOADERS) >> 2;
+    const uint32_t lead = cl_map(accempty, 0);
+    int done_tiles = 0;
+    for (int u = pair; walk.get(a, u, t); u += npairs, ++done_tiles) {
+      int good = 1;
+      if (lane == 0) good = !*abort_s && mbar_wait(accfull, done_tiles & 1) ? 1 : 0;
+      good = __shfl_sync(0xffffffffu, good, 0);
+      if (!good) {
+        if (lane == 0) *abort_s = 1;
+        break;
+      }
+      tc_fence_after();
+      const int64_t r = t.m0 + GH * (int64_t)rank + q * 32 + lane;
+      const float xg = !PART && a.xg ? *a.xg : 1.f, wg = !PART && a.wg ? a.wg[t.e] : 1.f;
+      const int groups = t.cols / 64;    // 32-column groups of this warp: half, half + 2, ...
+      const int64_t ld = PART ? a.m : a.ldy;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
+      if (BF16) {
+        uint32_t pk[4][16];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g < groups) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(acc + (uint32_t)(2 * g + half) * 32, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[2 * e]), xg), wg),
+                                                             __fmul_rn(__fmul_rn(__uint_as_float(v[2 * e + 1]), xg), wg));
+              pk[g][e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead);
+        uint16_t* y = static_cast<uint16_t*>(a.y);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g < groups) {
+            const int64_t tk = t.t0 + (2 * g + half) * 32;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (r < a.m && tk + 2 * e < t.t1) y[(tk + 2 * e) * ld + r] = (uint16_t)(pk[g][e] & 0xFFFFu);
+              if (r < a.m && tk + 2 * e + 1 < t.t1) y[(tk + 2 * e + 1) * ld + r] = (uint16_t)(pk[g][e] >> 16);
+            }
+          }
+        }
+      } else {
+        float* y = PART ? a.part + (int64_t)t.split * a.T * a.m : static_cast<float*>(a.y);
+#pragma unroll 1
+        for (int g = 0; g < groups; ++g) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(acc + (uint32_t)(2 * g + half) * 32, v);
+          tmem_wait_ld();
+          const int64_t tk = t.t0 + (2 * g + half) * 32;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (r < a.m && tk + e < t.t1) y[(tk + e) * ld + r] = __fmul_rn(__fmul_rn(__uint_as_float(v[e]), xg), wg);
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead);
+      }
+    }
+  }
+  if (*abort_s) {   // copies in flight land within microseconds; leave after a millisecond
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cl_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const GemmArgs);
+
+// Most pairs of the kernel that run at once on the current device (a property
+// of the device, asked for once per kernel), 0 on error.
+int active_pairs(Kernel fn, int which) {
+  static std::atomic<int> known[64][8];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int v = known[dev][which].load(std::memory_order_relaxed);
+  if (v > 0) return v;
+  if (allow_smem(reinterpret_cast<const void*>(fn), SMEM) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(2 * (sm_count() / 2)));
+  if (cudaOccupancyMaxActiveClusters(&v, reinterpret_cast<const void*>(fn), &cfg) != cudaSuccess || v < 1) return 0;
+  known[dev][which].store(v, std::memory_order_relaxed);
+  return v;
+}
+
+}  // namespace
+
+cudaError_t status_fetch_fp4(int* out, cudaStream_t s) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  const int zero = 0;
+  e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamSynchronize(s);
+  *out = v;
+  return e;
+}
+
+kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
+  const int64_t tiles_m = ceil_div(g.m, GM), tiles_t = ceil_div(g.T, GN) + (g.offsets ? g.E : 0);
+  if (tiles_m * tiles_t > (int64_t(1) << 30)) return fail(KRONQ_ERR_UNSUPPORTED, "fp4 product: more than 2^30 tiles");
+  CUtensorMap mw, mx;
+  const int64_t ldc = fp4_code_row(g.n), bytes = ceil_div(g.n, 2);
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if (!tma_map_2d(&mw, u8, 1, g.wc, bytes, (g.offsets ? g.E : 1) * g.m, ldc, 128, GH) ||
+      !tma_map_2d(&mx, u8, 1, g.xc, bytes, g.T, ldc, 128, XROWS))
+    return fail(KRONQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (fp4 product)");
+  GemmArgs a;
+  a.xs = g.xs; a.ws = g.ws; a.xg = g.xg; a.wg = g.wg;
+  a.offsets = g.offsets;
+  a.E = g.offsets ? (int)g.E : 1;
+  a.T = g.T; a.m = g.m;
+  a.lds = fp4_scale_row(fmt, g.n);
+  a.kb = (int)ceil_div(g.n, fp4_block(fmt));
+  a.nchunks = (int)ceil_div(g.n, CK);
+  a.tiles_m = (int)tiles_m;
+  a.splits = 1;
+  a.per_split = a.nchunks;
+  a.y = g.y; a.ldy = g.ldy; a.part = nullptr;
+  static const Kernel kernels[4] = {fp4_gemm_kernel<KRONQ_MXFP4, false, false>, fp4_gemm_kernel<KRONQ_MXFP4, true, false>,
+                                    fp4_gemm_kernel<KRONQ_NVFP4, false, false>, fp4_gemm_kernel<KRONQ_NVFP4, true, false>};
+  const int which = 2 * (fmt == KRONQ_NVFP4) + (g.y_bf16 ? 1 : 0);
+  const int pairs = active_pairs(kernels[which], which);
+  if (pairs < 1) return fail(KRONQ_ERR_CUDA, "fp4 product: no pair of SMs can run the kernel");
+  const int64_t most = tiles_m * tiles_t;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[which], mw, mx, a);
+  count_launch();
+  if (e != cudaSuccess) return cuda_fail(e, "fp4_gemm_kernel");
+  return KRONQ_OK;
+}
+
+}  // namespace kq

@@ -5,6 +5,7 @@
 // shared memory 32 columns at a time (E2M1 value times block scale, exact in
 // float32), float32 accumulation.
 #include "fp4.cuh"
+#include "fp4_gemm.h"
 #include "internal.h"
 
 namespace kq {
@@ -138,11 +139,8 @@ kronq_status kronq_fp4_matmul(const uint8_t* xc, const uint8_t* xs, const float*
   kronq_status r = check_product("fp4_matmul", fmt, T, m, n, xc, wc, ws, wg, y, ydt, ldy);
   if (r == KRONQ_OK) r = check_tokens("fp4_matmul", fmt, T, xc, xs, xg);
   if (r != KRONQ_OK || T == 0) return r;
-  SimpleArgs a{};
-  a.xc = xc; a.xs = xs; a.xg = xg; a.wc = wc; a.ws = ws; a.wg = wg;
-  a.T = T; a.m = m; a.n = n; a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
-  a.y = y; a.y_bf16 = ydt == KRONQ_BF16; a.ldy = ldy; a.E = 1;
-  return simple(a, fmt, as_stream(s));
+  Fp4Gemm g{xc, xs, xg, wc, ws, wg, T, m, n, y, ydt == KRONQ_BF16, ldy, nullptr, 1};
+  return fp4_gemm(g, fmt, as_stream(s));
 }
 
 size_t kronq_fp4_matvec_workspace_bytes(int64_t T, int64_t m, int64_t n, kronq_fp4_format fmt) {
@@ -180,11 +178,8 @@ kronq_status kronq_fp4_grouped_matmul(const uint8_t* xc, const uint8_t* xs, cons
   if (!offsets) return fail(KRONQ_ERR_INVALID_ARG, "fp4_grouped_matmul: NULL pointer");
   if (!aligned(offsets, 4)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_grouped_matmul: misaligned pointer");
   if (T == 0) return KRONQ_OK;
-  SimpleArgs a{};
-  a.xc = xc; a.xs = xs; a.xg = xg; a.wc = wc; a.ws = ws; a.wg = wg;
-  a.T = T; a.m = m; a.n = n; a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
-  a.y = y; a.y_bf16 = ydt == KRONQ_BF16; a.ldy = ldy; a.offsets = offsets; a.E = (int)E;
-  return simple(a, fmt, as_stream(s));
+  Fp4Gemm g{xc, xs, xg, wc, ws, wg, T, m, n, y, ydt == KRONQ_BF16, ldy, offsets, E};
+  return fp4_gemm(g, fmt, as_stream(s));
 }
 
 }  // extern "C"
