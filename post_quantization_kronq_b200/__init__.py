@@ -311,6 +311,11 @@ def kronq_kfac_loss(E, HG, ws=None, stream=None) -> float:
 
 
 # ------------------------------------------------------------ microscaled 4-bit floating point
+# These calls run once per layer and decoded token, so their marshalling is
+# kept short: plain integers for pointers, sizes worked out here.
+_FP4_ROW_DIVISOR = (512, 256)    # columns of 16 scale bytes: MXFP4, NVFP4
+
+
 def kronq_fp4_code_row_bytes(n: int) -> int:
     return int(lib.kronq_fp4_code_row_bytes(n))
 
@@ -322,56 +327,66 @@ def kronq_fp4_scale_row_bytes(fmt: int, n: int) -> int:
 def _fp4_call(fn, device, stream, *args):
     """One library call with the tensors' device current, on the given stream or that device's current one."""
     import torch
-    if stream is not None and stream.device != device:
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
         raise ValueError(f"stream of {stream.device} for tensors on {device}")
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            check(fn(*args, _stream(stream)))
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
     else:
-        check(fn(*args, _stream(stream)))
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    check(status)
 
 
-def _fp4_rows(t, name):
-    """A two-dimensional device matrix whose rows are dense (any row stride)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def _fp4_matrix(t, name):
+    """(pointer, rows, columns, row stride) of a device matrix with dense rows."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be a matrix with unit stride along its rows")
     if not t.is_cuda:
         raise ValueError(f"{name} must live in device memory")
-    return t
+    rows, n = shape
+    return t.data_ptr(), rows, n, stride[0] if rows > 1 else max(stride[0], n)
 
 
-def _fp4_ld(t):
-    """Row stride in elements (a single row may carry any stride)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _fp4_bytes(t, name, shape, device):
-    import torch
-    if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous uint8 of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must live on {device}")
+def _fp4_pair(codes, scales, name, fmt, lead, n, device):
+    """Pointers of a quantised matrix's codes and scales, whose shapes are lead + (row bytes,)."""
+    if fmt != MXFP4 and fmt != NVFP4:
+        raise ValueError("fmt must be MXFP4 or NVFP4")
+    for t, what, width in ((codes, "codes", (n + 31) // 32 * 16),
+                           (scales, "scales", -(-n // _FP4_ROW_DIVISOR[fmt]) * 16)):
+        if t.element_size() != 1 or t.is_floating_point() or t.shape != lead + (width,) or not t.is_contiguous():
+            raise ValueError(f"{name} {what} must be contiguous uint8 of shape {lead + (width,)}, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} {what} must live on {device}")
+    return codes.data_ptr(), scales.data_ptr()
 
 
 def _fp4_scale(t, name, fmt, count, device):
+    if t is None:
+        if fmt == NVFP4:
+            raise ValueError(f"{name}: NVFP4 has a float32 tensor scale")
+        return None
+    if fmt != NVFP4:
+        raise ValueError(f"{name}: MXFP4 has no tensor scale")
     import torch
-    if (t is None) == (fmt == NVFP4):
-        raise ValueError(f"{name}: a float32 tensor scale goes with NVFP4 and with it only")
-    if t is not None and (t.dtype != torch.float32 or t.numel() != count or t.device != device
-                          or not t.is_contiguous()):
+    if t.dtype != torch.float32 or t.numel() != count or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must hold {count} float32 on {device}")
+    return t.data_ptr()
 
 
-def _fp4_ws(ws, need, device):
+def _fp4_ws(ws, need, args, device):
+    """(pointer, bytes, owner) of the workspace; allocated where none is given and one is needed."""
     if ws is None:
-        return workspace(need, device) if need else None
-    if ws.device != device or not ws.is_contiguous():
+        nbytes = need(*args)
+        if nbytes == 0:
+            return None, 0, None
+        ws = workspace(nbytes, device)
+    elif ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous on {device}")
-    return ws
-
-
-def _fp4_ws_args(ws):
-    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def kronq_fp4_quantize_workspace_bytes(rows: int, n: int, fmt: int) -> int:
@@ -382,35 +397,29 @@ def kronq_fp4_quantize(x, fmt: int, codes, scales, gscale=None, gscale_given: bo
                        stream=None):
     """codes, scales (and NVFP4's gscale, unless given) of x (rows x n, bf16 or
     float32, dense rows); deq (x's type) receives the values they stand for."""
-    _fp4_rows(x, "x")
-    rows, n = x.shape
+    px, rows, n, ldx = _fp4_matrix(x, "x")
     dev = x.device
-    _fp4_bytes(codes, "codes", (rows, kronq_fp4_code_row_bytes(n)), dev)
-    _fp4_bytes(scales, "scales", (rows, kronq_fp4_scale_row_bytes(fmt, n)), dev)
-    _fp4_scale(gscale, "gscale", fmt, 1, dev)
+    pc, ps = _fp4_pair(codes, scales, "output", fmt, (rows,), n, dev)
+    pg = _fp4_scale(gscale, "gscale", fmt, 1, dev)
+    pd, ldd = None, 0
     if deq is not None:
-        _fp4_rows(deq, "deq")
+        pd, _, _, ldd = _fp4_matrix(deq, "deq")
         if deq.shape != x.shape or deq.dtype != x.dtype or deq.device != dev:
             raise ValueError("deq must have x's shape, type and device")
-    if fmt == NVFP4 and not gscale_given:
-        ws = _fp4_ws(ws, kronq_fp4_quantize_workspace_bytes(rows, n, fmt), dev)
-    else:
-        ws = None
-    _fp4_call(lib.kronq_fp4_quantize, dev, stream, _ptr(x), _dtype_code(x), rows, n, _fp4_ld(x), fmt, _ptr(codes),
-              _ptr(scales), _ptr(gscale), 1 if gscale_given else 0, _ptr(deq), 0 if deq is None else _fp4_ld(deq),
-              *_fp4_ws_args(ws))
+    pw, nw = None, 0
+    if pg is not None and not gscale_given:
+        pw, nw, ws = _fp4_ws(ws, kronq_fp4_quantize_workspace_bytes, (rows, n, fmt), dev)
+    _fp4_call(lib.kronq_fp4_quantize, dev, stream, px, _dtype_code(x), rows, n, ldx, fmt, pc, ps, pg,
+              1 if gscale_given else 0, pd, ldd, pw, nw)
 
 
 def kronq_fp4_dequantize(codes, scales, fmt: int, out, gscale=None, stream=None):
     """out (rows x n, bf16 or float32, dense rows) = the values of codes and scales."""
-    _fp4_rows(out, "out")
-    rows, n = out.shape
+    po, rows, n, ldo = _fp4_matrix(out, "out")
     dev = out.device
-    _fp4_bytes(codes, "codes", (rows, kronq_fp4_code_row_bytes(n)), dev)
-    _fp4_bytes(scales, "scales", (rows, kronq_fp4_scale_row_bytes(fmt, n)), dev)
-    _fp4_scale(gscale, "gscale", fmt, 1, dev)
-    _fp4_call(lib.kronq_fp4_dequantize, dev, stream, _ptr(codes), _ptr(scales), _ptr(gscale), fmt, rows, n, _ptr(out),
-              _dtype_code(out), _fp4_ld(out))
+    pc, ps = _fp4_pair(codes, scales, "input", fmt, (rows,), n, dev)
+    pg = _fp4_scale(gscale, "gscale", fmt, 1, dev)
+    _fp4_call(lib.kronq_fp4_dequantize, dev, stream, pc, ps, pg, fmt, rows, n, po, _dtype_code(out), ldo)
 
 
 def kronq_fp4_matmul_workspace_bytes(T: int, m: int, n: int, fmt: int) -> int:
@@ -420,16 +429,14 @@ def kronq_fp4_matmul_workspace_bytes(T: int, m: int, n: int, fmt: int) -> int:
 def kronq_fp4_matmul(xc, xs, wc, wsc, fmt: int, n: int, y, xg=None, wg=None, ws=None, stream=None):
     """y (T x m, bf16 or float32, dense rows) = X W^T for quantised X (T x n)
     and W (m x n), each as codes, scales and (NVFP4) a tensor scale."""
-    _fp4_rows(y, "y")
-    T, m = y.shape
+    py, T, m, ldy = _fp4_matrix(y, "y")
     dev = y.device
-    lc, ls = kronq_fp4_code_row_bytes(n), kronq_fp4_scale_row_bytes(fmt, n)
-    _fp4_bytes(xc, "xc", (T, lc), dev), _fp4_bytes(xs, "xs", (T, ls), dev)
-    _fp4_bytes(wc, "wc", (m, lc), dev), _fp4_bytes(wsc, "wsc", (m, ls), dev)
-    _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, 1, dev)
-    ws = _fp4_ws(ws, kronq_fp4_matmul_workspace_bytes(T, m, n, fmt) if ws is None else 0, dev)
-    _fp4_call(lib.kronq_fp4_matmul, dev, stream, _ptr(xc), _ptr(xs), _ptr(xg), _ptr(wc), _ptr(wsc), _ptr(wg), fmt, T,
-              m, n, _ptr(y), _dtype_code(y), _fp4_ld(y), *_fp4_ws_args(ws))
+    pxc, pxs = _fp4_pair(xc, xs, "X", fmt, (T,), n, dev)
+    pwc, pws = _fp4_pair(wc, wsc, "W", fmt, (m,), n, dev)
+    pxg, pwg = _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, 1, dev)
+    pw, nw, ws = _fp4_ws(ws, kronq_fp4_matmul_workspace_bytes, (T, m, n, fmt), dev)
+    _fp4_call(lib.kronq_fp4_matmul, dev, stream, pxc, pxs, pxg, pwc, pws, pwg, fmt, T, m, n, py, _dtype_code(y),
+              ldy, pw, nw)
 
 
 def kronq_fp4_matvec_workspace_bytes(T: int, m: int, n: int, fmt: int) -> int:
@@ -439,18 +446,16 @@ def kronq_fp4_matvec_workspace_bytes(T: int, m: int, n: int, fmt: int) -> int:
 def kronq_fp4_matvec(x, wc, wsc, fmt: int, y, wg=None, ws=None, stream=None):
     """y (T x m, bf16 or float32) = X W^T for at most 16 tokens X (T x n, bf16
     or float32, not quantised) and quantised W (m x n)."""
-    _fp4_rows(x, "x"), _fp4_rows(y, "y")
-    T, n = x.shape
-    m = y.shape[1]
+    px, T, n, ldx = _fp4_matrix(x, "x")
+    py, Ty, m, ldy = _fp4_matrix(y, "y")
     dev = y.device
-    if y.shape[0] != T or x.device != dev:
+    if Ty != T or x.device != dev:
         raise ValueError("x and y must have the same rows and device")
-    _fp4_bytes(wc, "wc", (m, kronq_fp4_code_row_bytes(n)), dev)
-    _fp4_bytes(wsc, "wsc", (m, kronq_fp4_scale_row_bytes(fmt, n)), dev)
-    _fp4_scale(wg, "wg", fmt, 1, dev)
-    ws = _fp4_ws(ws, kronq_fp4_matvec_workspace_bytes(T, m, n, fmt) if ws is None else 0, dev)
-    _fp4_call(lib.kronq_fp4_matvec, dev, stream, _ptr(x), _dtype_code(x), _fp4_ld(x), _ptr(wc), _ptr(wsc), _ptr(wg),
-              fmt, T, m, n, _ptr(y), _dtype_code(y), _fp4_ld(y), *_fp4_ws_args(ws))
+    pwc, pws = _fp4_pair(wc, wsc, "W", fmt, (m,), n, dev)
+    pwg = _fp4_scale(wg, "wg", fmt, 1, dev)
+    pw, nw, ws = _fp4_ws(ws, kronq_fp4_matvec_workspace_bytes, (T, m, n, fmt), dev)
+    _fp4_call(lib.kronq_fp4_matvec, dev, stream, px, _dtype_code(x), ldx, pwc, pws, pwg, fmt, T, m, n, py,
+              _dtype_code(y), ldy, pw, nw)
 
 
 def kronq_fp4_grouped_matmul(xc, xs, offsets, wc, wsc, fmt: int, n: int, y, xg=None, wg=None, stream=None):
@@ -458,15 +463,13 @@ def kronq_fp4_grouped_matmul(xc, xs, offsets, wc, wsc, fmt: int, n: int, y, xg=N
     weights: wc, wsc (E x m x row bytes), wg (E float32, NVFP4), offsets
     (E + 1 int32).  Rows of no group are left as they were."""
     import torch
-    _fp4_rows(y, "y")
-    T, m = y.shape
+    py, T, m, ldy = _fp4_matrix(y, "y")
     dev = y.device
     E = offsets.numel() - 1
     if offsets.dtype != torch.int32 or offsets.device != dev or not offsets.is_contiguous():
         raise ValueError(f"offsets must be contiguous int32 on {dev}")
-    lc, ls = kronq_fp4_code_row_bytes(n), kronq_fp4_scale_row_bytes(fmt, n)
-    _fp4_bytes(xc, "xc", (T, lc), dev), _fp4_bytes(xs, "xs", (T, ls), dev)
-    _fp4_bytes(wc, "wc", (E, m, lc), dev), _fp4_bytes(wsc, "wsc", (E, m, ls), dev)
-    _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, E, dev)
-    _fp4_call(lib.kronq_fp4_grouped_matmul, dev, stream, _ptr(xc), _ptr(xs), _ptr(xg), _ptr(offsets), E, _ptr(wc),
-              _ptr(wsc), _ptr(wg), fmt, T, m, n, _ptr(y), _dtype_code(y), _fp4_ld(y))
+    pxc, pxs = _fp4_pair(xc, xs, "X", fmt, (T,), n, dev)
+    pwc, pws = _fp4_pair(wc, wsc, "W", fmt, (E, m), n, dev)
+    pxg, pwg = _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, E, dev)
+    _fp4_call(lib.kronq_fp4_grouped_matmul, dev, stream, pxc, pxs, pxg, offsets.data_ptr(), E, pwc, pws, pwg, fmt, T,
+              m, n, py, _dtype_code(y), ldy)

@@ -9,7 +9,7 @@
 #include <vector>
 
 #include "common.cuh"
-#include "fp4_gemm.h"
+#include "fp4_products.h"
 #include "internal.h"
 
 namespace kq {

@@ -1,98 +1,13 @@
-// Products of microscaled 4-bit matrices: y = A W^T with both operands
-// quantised, with full-precision tokens (a few rows), and grouped by expert.
-//
-// First form: one 64 x 64 tile of y per CTA, both operands dequantised into
-// shared memory 32 columns at a time (E2M1 value times block scale, exact in
-// float32), float32 accumulation.
+// C entry points of the products of microscaled 4-bit matrices: argument
+// checks, then the kernels of fp4_gemm.cu and fp4_matvec.cu.
 #include "fp4.cuh"
-#include "fp4_gemm.h"
+#include "fp4_products.h"
 #include "internal.h"
 
 namespace kq {
 namespace {
 
-constexpr int TT = 64, TM = 64, TK = 32;
-
-struct SimpleArgs {
-  const uint8_t *xc, *xs;   // quantised tokens, or
-  const void* x;            // full-precision tokens
-  int x_bf16;
-  int64_t ldx;
-  const float *xg, *wg;
-  const uint8_t *wc, *ws;
-  int64_t T, m, n, ldc, lds;
-  void* y;
-  int y_bf16;
-  int64_t ldy;
-  const int* offsets;       // grouped: E + 1
-  int E;
-};
-
-template <int FMT>
-__device__ __forceinline__ float fp4_at(const uint8_t* codes, const uint8_t* scales, int64_t r, int64_t k, int64_t ldc,
-                                        int64_t lds) {
-  const uint32_t b = codes[r * ldc + (k >> 1)];
-  const float2 v = e2m1x2_float2(b);
-  return ((k & 1) ? v.y : v.x) * fp4_scale_value<FMT>(scales[r * lds + k / (FMT == KRONQ_MXFP4 ? 32 : 16)]);
-}
-
-template <int FMT>
-__global__ void __launch_bounds__(256) fp4_simple_kernel(const SimpleArgs a) {
-  __shared__ float xs[TK][TT + 1], wsm[TK][TM + 1];
-  const int e = blockIdx.z;
-  int64_t t_lo = 0, t_hi = a.T;
-  if (a.offsets) {
-    int64_t lo = 0;
-    for (int i = 0; i <= e; ++i) lo = max(lo, min((int64_t)max(a.offsets[i], 0), a.T));
-    t_lo = lo;
-    t_hi = max(lo, min((int64_t)max(a.offsets[e + 1], 0), a.T));
-  }
-  const int64_t t0 = t_lo + (int64_t)blockIdx.y * TT, m0 = (int64_t)blockIdx.x * TM;
-  if (t0 >= t_hi) return;
-  const uint8_t* wc = a.wc + (int64_t)e * a.m * a.ldc;
-  const uint8_t* wsc = a.ws + (int64_t)e * a.m * a.lds;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < a.n; k0 += TK) {
-    for (int i = threadIdx.x; i < TT * TK; i += 256) {
-      const int r = i / TK, k = i % TK;
-      float v = 0.f;
-      if (t0 + r < t_hi && k0 + k < a.n) {
-        if (a.x) v = a.x_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.x)[(t0 + r) * a.ldx + k0 + k])
-                              : static_cast<const float*>(a.x)[(t0 + r) * a.ldx + k0 + k];
-        else v = fp4_at<FMT>(a.xc, a.xs, t0 + r, k0 + k, a.ldc, a.lds);
-      }
-      xs[k][r] = v;
-      wsm[k][r] = (m0 + r < a.m && k0 + k < a.n) ? fp4_at<FMT>(wc, wsc, m0 + r, k0 + k, a.ldc, a.lds) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < TK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[k][ty * 4 + i], wsm[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = t0 + ty * 4 + i, r = m0 + tx + 16 * j;
-      if (t >= t_hi || r >= a.m) continue;
-      float v = acc[i][j];
-      if (a.xg) v *= *a.xg;
-      if (a.wg) v *= a.wg[e];
-      if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + r] = __float2bfloat16_rn(v);
-      else static_cast<float*>(a.y)[t * a.ldy + r] = v;
-    }
-}
-
-kronq_status simple(const SimpleArgs& a, int fmt, cudaStream_t st) {
-  dim3 grid((unsigned)ceil_div(a.m, TM), (unsigned)ceil_div(a.T, TT), (unsigned)a.E);
-  if (fmt == KRONQ_MXFP4) fp4_simple_kernel<KRONQ_MXFP4><<<grid, 256, 0, st>>>(a);
-  else fp4_simple_kernel<KRONQ_NVFP4><<<grid, 256, 0, st>>>(a);
-  KQ_LAUNCH_CHECK("fp4_simple_kernel");
-  return KRONQ_OK;
-}
+constexpr int64_t kMatvecMaxN = int64_t(1) << 24;   // column slices are a grid dimension
 
 // The checks that the three products share; name is the caller's.
 kronq_status check_product(const char* name, int fmt, int64_t T, int64_t m, int64_t n, const void* x, const void* wc,
@@ -144,7 +59,10 @@ kronq_status kronq_fp4_matmul(const uint8_t* xc, const uint8_t* xs, const float*
 }
 
 size_t kronq_fp4_matvec_workspace_bytes(int64_t T, int64_t m, int64_t n, kronq_fp4_format fmt) {
-  return 0;
+  if (!fp4_fmt_ok(fmt) || T <= 0 || T > KRONQ_FP4_MATVEC_MAX_TOKENS || m <= 0 || m > kFp4MaxDim || n <= 0 ||
+      n > kMatvecMaxN)
+    return 0;
+  return fp4_matvec_workspace(T, m, n);
 }
 
 kronq_status kronq_fp4_matvec(const void* x, kronq_dtype xdt, int64_t ldx, const uint8_t* wc, const uint8_t* ws,
@@ -155,14 +73,15 @@ kronq_status kronq_fp4_matvec(const void* x, kronq_dtype xdt, int64_t ldx, const
   if (xdt != KRONQ_BF16 && xdt != KRONQ_F32) return fail(KRONQ_ERR_INVALID_ARG, "fp4_matvec: bad dtype");
   if (T > KRONQ_FP4_MATVEC_MAX_TOKENS)
     return fail(KRONQ_ERR_UNSUPPORTED, "fp4_matvec: more than KRONQ_FP4_MATVEC_MAX_TOKENS tokens");
+  if (n > kMatvecMaxN) return fail(KRONQ_ERR_UNSUPPORTED, "fp4_matvec: row too long");
   if (ldx < n) return fail(KRONQ_ERR_INVALID_ARG, "fp4_matvec: row stride of x below n");
   if (!aligned(x, xdt == KRONQ_BF16 ? 2 : 4)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_matvec: misaligned pointer");
   if (T == 0) return KRONQ_OK;
-  SimpleArgs a{};
-  a.x = x; a.x_bf16 = xdt == KRONQ_BF16; a.ldx = ldx; a.wc = wc; a.ws = ws; a.wg = wg;
-  a.T = T; a.m = m; a.n = n; a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
-  a.y = y; a.y_bf16 = ydt == KRONQ_BF16; a.ldy = ldy; a.E = 1;
-  return simple(a, fmt, as_stream(s));
+  const size_t need = fp4_matvec_workspace(T, m, n);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+    return fail(KRONQ_ERR_INVALID_ARG, "fp4_matvec: workspace too small or not 256-byte aligned");
+  Fp4Matvec v{x, xdt == KRONQ_F32, ldx, wc, ws, wg, T, m, n, y, ydt == KRONQ_BF16, ldy, workspace};
+  return fp4_matvec(v, fmt, as_stream(s));
 }
 
 kronq_status kronq_fp4_grouped_matmul(const uint8_t* xc, const uint8_t* xs, const float* xg, const int* offsets,

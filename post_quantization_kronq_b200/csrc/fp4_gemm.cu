@@ -27,7 +27,7 @@
 #include <atomic>
 
 #include "fp4.cuh"
-#include "fp4_gemm.h"
+#include "fp4_products.h"
 #include "internal.h"
 
 namespace kq {
