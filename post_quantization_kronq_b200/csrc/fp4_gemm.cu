@@ -14,13 +14,20 @@
 // words with row r in lane r % 32, word r / 32.  The user's layout is row by
 // row, so four loader warps read 16 bytes of four rows 32 apart, transpose
 // the 4 x 4 words in registers and store 16-byte rows of four such 512-byte
-// atoms; tcgen05.cp spreads an atom over TMEM.  A loader step covers 64 bytes
-// of scales of every row (1024 or 2048 columns), double-buffered.  A tile of
-// 256 x 256 leaves 256 of the 512 TMEM columns for scales; the eight epilogue
-// warps drain the accumulator into registers first and release it before they
+// atoms; tcgen05.cp spreads an atom over TMEM, one chunk ahead of its MMAs.
+// A loader step covers 64 bytes of scales of every row (1024 or 2048
+// columns); two sets of four warps take turns at the steps, because a global
+// load's latency is about as long as the MMAs of a step.  A tile of 256 x 256
+// leaves 256 of the 512 TMEM columns for scales; the eight epilogue warps
+// drain the accumulator into registers first and release it before they
 // store.
 //
-// Warps: 0 TMA, 1 MMA (lane 0 of the even CTA), 2-5 scales, 6-13 epilogue.
+// The even CTA's MMA thread must know of the odd CTA's scales.  An arrival at
+// another CTA's barrier that releases shared memory writes takes 1500 - 2200
+// cycles, so the loaders arrive at their own CTA's barrier and the odd CTA's
+// otherwise idle warp 1 hands the arrival on.
+//
+// Warps: 0 TMA, 1 MMA (one lane of the even CTA), 2-9 scales, 10-17 epilogue.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -44,8 +51,8 @@ constexpr int STAGE = WBOX + GH * 128;        // 32 KB
 constexpr int PIECE = 3 * 2048;               // 16 scale bytes of 128 + 256 rows, as atoms
 constexpr int SFBUF = 4 * PIECE;              // one loader step
 constexpr int GROUP_INTS = 2 * (KRONQ_FP4_MAX_EXPERTS + 1);
-constexpr int THREADS = 448;
-constexpr int LOADERS = 4, EPI = 8;
+constexpr int LOADERS = 4, EPI = 8;           // warps of a loader set (of two), of the epilogue
+constexpr int THREADS = 32 * (2 + 2 * LOADERS + EPI);
 constexpr int SMEM = STAGES * STAGE + 2 * SFBUF + 256 + GROUP_INTS * 4 + 1024;
 constexpr uint32_t SF_COL = GN;               // TMEM columns of the scales: 4 chunks of 48
 
@@ -145,6 +152,15 @@ __device__ void group_walk(const GemmArgs& a, int* bound, int* first, int lane) 
   if (lane == 0) first[a.E] = sum;
 }
 
+// 32 lanes x 16 consecutive 32-bit columns: thread t gets lane (base + t).
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+
 // Descriptor of a 512-byte scale atom: no swizzle, 8-row groups of 16-byte rows.
 __device__ __forceinline__ uint64_t atom_desc(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
@@ -152,6 +168,22 @@ __device__ __forceinline__ uint64_t atom_desc(uint32_t saddr) {
 }
 __device__ __forceinline__ void copy_atom(uint32_t tcol, uint32_t saddr) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tcol), "l"(atom_desc(saddr)) : "memory");
+}
+
+// One lane of a converged warp, in the form from which the compiler knows that
+// a single thread issues (a test of the lane number costs tens of cycles per
+// tcgen05 instruction).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Arrival at a barrier of the pair that hands over no memory writes (the
+// accumulator's columns, read by tcgen05.ld that has completed), so without
+// the release at cluster scope.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 template <int FMT>
@@ -212,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(sffull0 + 8 * b, 2 * LOADERS);
+      mbar_init(sffull0 + 8 * b, rank == 0 ? LOADERS + 1 : LOADERS);
       mbar_init(sfempty0 + 8 * b, 1);
     }
     mbar_init(accfull, 1);
@@ -239,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   Tile t;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_lane()) {
       const uint32_t full_lead = cl_map(full0, 0);
       uint32_t it = 0;
       bool ok = true;
@@ -264,40 +296,46 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
-      uint32_t it = 0, sit = 0;
+    if (rank == 0 && elect_lane()) {
+      uint32_t it = 0, cit = 0, sit = 0;   // chunks multiplied, chunks whose scales are copied, loader steps
       int done_tiles = 0;
       bool ok = true, issued = false;
-      for (int u = pair; ok && walk.get(a, u, t); u += npairs, ++done_tiles) {
-        if (done_tiles > 0 && (*abort_s || !mbar_wait(accempty, (done_tiles - 1) & 1))) {
-          *abort_s = 1;
-          break;
-        }
+      // scales of the unit's local chunk lc into TMEM; the step's buffer is
+      // free once its last copy has run
+      auto copy_scales = [&](int lc, bool last) -> bool {
+        const int in = lc % CPS;
+        if (in == 0 && (*abort_s || !mbar_wait(sffull0 + 8 * (sit & 1), (sit >> 1) & 1))) return false;
         tc_fence_after();
-        const int halves = (t.cols + GH - 1) / GH;
-        for (int c = t.c0; c < t.c1; ++c, ++it) {
-          const int lc = c - t.c0, in = lc % CPS;
-          if (in == 0 && (*abort_s || !mbar_wait(sffull0 + 8 * (sit & 1), (sit >> 1) & 1))) {
-            *abort_s = 1;
-            ok = false;
-            break;
-          }
-          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
-          if (*abort_s || !mbar_wait(full0 + 8 * s, ph)) {
-            *abort_s = 1;
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t piece = smem_u32(sfmem) + (sit & 1) * SFBUF + (in / CPP) * PIECE;
-          const uint32_t sf = tmem + SF_COL + (it & 3) * 48;
+        const uint32_t piece = smem_u32(sfmem) + (sit & 1) * SFBUF + (in / CPP) * PIECE;
+        const uint32_t sf = tmem + SF_COL + (cit & 3) * 48;
+        const bool two = t.cols > GH;
 #pragma unroll
-          for (int j = 0; j < 4 / CPP; ++j) {
-            const uint32_t atom = piece + (CPP == 1 ? j : 2 * (in & 1) + j) * 512;
-            copy_atom(sf + 4 * j, atom);
-            copy_atom(sf + 16 + 8 * j, atom + 2048);
-            if (halves > 1) copy_atom(sf + 20 + 8 * j, atom + 4096);
-          }
+        for (int j = 0; j < 4 / CPP; ++j) {
+          const uint32_t atom = piece + (CPP == 1 ? j : 2 * (in & 1) + j) * 512;
+          copy_atom(sf + 4 * j, atom);
+          copy_atom(sf + 16 + 8 * j, atom + 2048);
+          if (two) copy_atom(sf + 20 + 8 * j, atom + 4096);
+        }
+        issued = true;
+        if (in == CPS - 1 || last) {
+          mma_commit_pair_mc(sfempty0 + 8 * (sit & 1), 0x3);
+          ++sit;
+        }
+        ++cit;
+        return true;
+      };
+      for (int u = pair; ok && walk.get(a, u, t); u += npairs, ++done_tiles) {
+        const int count = t.c1 - t.c0;
+        ok = copy_scales(0, count == 1);
+        if (ok && done_tiles > 0) ok = !*abort_s && mbar_wait(accempty, (done_tiles - 1) & 1);
+        tc_fence_after();
+        for (int lc = 0; ok && lc < count; ++lc, ++it) {
+          if (lc + 1 < count) ok = copy_scales(lc + 1, lc + 2 == count);
+          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
+          ok = ok && !*abort_s && mbar_wait(full0 + 8 * s, ph);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sf = tmem + SF_COL + (it & 3) * 48;
           const uint32_t st = smem_u32(smem) + s * STAGE;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
@@ -307,46 +345,48 @@ __global__ void __launch_bounds__(THREADS, 1)
                               fp4_idesc<FMT>(t.cols, CPP == 1 ? 0u : 2u * (kk & 1)), sf + 4 * j, sf + 16 + 8 * j,
                               (lc | kk) != 0 ? 1u : 0u);
           }
-          issued = true;
           mma_commit_pair_mc(empty0 + 8 * s, 0x3);
-          if (in == CPS - 1 || c + 1 == t.c1) {
-            mma_commit_pair_mc(sfempty0 + 8 * (sit & 1), 0x3);
-            ++sit;
-          }
         }
         if (ok) mma_commit_pair_mc(accfull, 0x3);
       }
+      if (!ok) *abort_s = 1;
       if (issued) {
         mma_commit_pair_mc(done, 0x1);
         mbar_wait(done, 0);
       }
+    } else if (rank == 1 && elect_lane()) {
+      const uint32_t lead = cl_map(sffull0, 0);
+      uint32_t sit = 0;
+      bool ok = true;
+      for (int u = pair; ok && walk.get(a, u, t); u += npairs)
+        for (int c = t.c0; ok && c < t.c1; c += CPS, ++sit) {
+          ok = !*abort_s && mbar_wait(sffull0 + 8 * (sit & 1), (sit >> 1) & 1);
+          if (ok) mbar_arrive_cluster(lead + 8 * (sit & 1));
+        }
+      if (!ok) *abort_s = 1;
     }
     __syncwarp();
-  } else if (warp < 2 + LOADERS) {
-    const int i = 8 * (warp - 2) + (lane & 7), p = lane >> 3;   // row modulo 32, piece of the step
-    const uint32_t lead = cl_map(sffull0, 0);
+  } else if (warp < 2 + 2 * LOADERS) {
+    const int set = (warp - 2) / LOADERS;
+    const int i = 8 * ((warp - 2) % LOADERS) + (lane & 7), p = lane >> 3;   // row modulo 32, piece of the step
     uint32_t sit = 0;
     bool ok = true;
     const int64_t wlast = (int64_t)a.E * a.m - 1;
     for (int u = pair; ok && walk.get(a, u, t); u += npairs) {
       const int halves = (t.cols + GH - 1) / GH;
-      // rows beyond the matrices read its last row: their results are not stored
-      const uint8_t* row[12];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t r = (int64_t)t.e * a.m + t.m0 + GH * (int64_t)rank + i + 32 * q;
-        row[q] = a.ws + min(r, wlast) * a.lds;
-        row[4 + q] = a.xs + min(t.t0 + i + 32 * q, a.T - 1) * a.lds;
-        row[8 + q] = a.xs + min(t.t0 + GH + i + 32 * q, a.T - 1) * a.lds;
-      }
+      // rows beyond the matrices read the last one: their results are not stored
+      const int64_t rw = (int64_t)t.e * a.m + t.m0 + GH * (int64_t)rank + i;
       for (int c = t.c0; c < t.c1; c += CPS, ++sit) {
+        if ((int)(sit & 1) != set) continue;
         const int byte = 16 * (c / CPP + p);
         const int valid = a.kb - byte;
         uint4 v[12];
 #pragma unroll
-        for (int q = 0; q < 12; ++q)
-          v[q] = valid > 0 && (q < 8 || halves > 1) ? __ldg(reinterpret_cast<const uint4*>(row[q] + byte))
+        for (int q = 0; q < 12; ++q) {
+          const uint8_t* row = q < 4 ? a.ws + min(rw + 32 * q, wlast) * a.lds : a.xs + min(t.t0 + i + 32 * (q - 4), a.T - 1) * a.lds;
+          v[q] = valid > 0 && (q < 8 || halves > 1) ? __ldg(reinterpret_cast<const uint4*>(row + byte))
                                                     : make_uint4(0, 0, 0, 0);
+        }
         if (valid > 0 && valid < 16) {
 #pragma unroll
           for (int q = 0; q < 12; ++q) {
@@ -377,11 +417,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead + 8 * (sit & 1));
+        if (lane == 0) mbar_arrive(sffull0 + 8 * (sit & 1));
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2 - LOADERS) >> 2;
+    const int q = warp & 3, half = (warp - 2 - 2 * LOADERS) >> 2;
     const uint32_t lead = cl_map(accempty, 0);
     int done_tiles = 0;
     for (int u = pair; walk.get(a, u, t); u += npairs, ++done_tiles) {
@@ -403,20 +443,23 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           if (g < groups) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(acc + (uint32_t)(2 * g + half) * 32, v);
-            tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[2 * e]), xg), wg),
-                                                             __fmul_rn(__fmul_rn(__uint_as_float(v[2 * e + 1]), xg), wg));
-              pk[g][e] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(acc + (uint32_t)(2 * g + half) * 32 + 16 * c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[2 * e]), xg), wg),
+                                                               __fmul_rn(__fmul_rn(__uint_as_float(v[2 * e + 1]), xg), wg));
+                pk[g][8 * c + e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead);
+        if (lane == 0) mbar_arrive_remote(lead);
         uint16_t* y = static_cast<uint16_t*>(a.y);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -444,7 +487,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead);
+        if (lane == 0) mbar_arrive_remote(lead);
       }
     }
   }
