@@ -12,22 +12,23 @@
 //
 // Scales: the tensor core wants, for 128 rows and 4 scale bytes, 32 lanes x 4
 // words with row r in lane r % 32, word r / 32.  The user's layout is row by
-// row, so four loader warps read 16 bytes of four rows 32 apart, transpose
+// row, so loader warps read 16 bytes of four rows 32 apart, transpose
 // the 4 x 4 words in registers and store 16-byte rows of four such 512-byte
 // atoms; tcgen05.cp spreads an atom over TMEM, one chunk ahead of its MMAs.
-// A loader step covers 64 bytes of scales of every row (1024 or 2048
-// columns); two sets of four warps take turns at the steps, because a global
-// load's latency is about as long as the MMAs of a step.  A tile of 256 x 256
+// They work in groups of two such pieces (32 bytes of scales of a row), four
+// groups in flight in registers and four in shared memory, because a load, its
+// way to the barrier and the copy take longer than the MMAs of a few chunks.  A tile of 256 x 256
 // leaves 256 of the 512 TMEM columns for scales; the eight epilogue warps
 // drain the accumulator into registers first and release it before they
 // store.
 //
-// The even CTA's MMA thread must know of the odd CTA's scales.  An arrival at
-// another CTA's barrier that releases shared memory writes takes 1500 - 2200
-// cycles, so the loaders arrive at their own CTA's barrier and the odd CTA's
-// otherwise idle warp 1 hands the arrival on.
+// The odd CTA's loaders arrive at the even CTA's barrier, whose MMA thread
+// copies the scales of both.  The arrival does not release at cluster scope
+// (that takes 1500 - 2200 cycles): what it announces is read by the async
+// proxy of the writer's own CTA, and each writer's proxy fence has made it
+// visible there before the arrival is issued.
 //
-// Warps: 0 TMA, 1 MMA (one lane of the even CTA), 2-9 scales, 10-17 epilogue.
+// Warps: 0 TMA, 1 MMA (one lane of the even CTA), 2-7 scales, 8-15 epilogue.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -49,11 +50,12 @@ constexpr int XBOX = XROWS * 128;             // 4 KB
 constexpr int STAGES = 5;
 constexpr int STAGE = WBOX + GH * 128;        // 32 KB
 constexpr int PIECE = 3 * 2048;               // 16 scale bytes of 128 + 256 rows, as atoms
-constexpr int SFBUF = 4 * PIECE;              // one loader step
+constexpr int SLOT = 2 * PIECE, SLOTS = 4;    // a loader group; groups in shared memory
+constexpr int AHEAD = 4;                      // groups in a loader's registers
 constexpr int GROUP_INTS = 2 * (KRONQ_FP4_MAX_EXPERTS + 1);
-constexpr int LOADERS = 4, EPI = 8;           // warps of a loader set (of two), of the epilogue
-constexpr int THREADS = 32 * (2 + 2 * LOADERS + EPI);
-constexpr int SMEM = STAGES * STAGE + 2 * SFBUF + 256 + GROUP_INTS * 4 + 1024;
+constexpr int LOADERS = 6, EPI = 8;           // warps
+constexpr int THREADS = 32 * (2 + LOADERS + EPI);
+constexpr int SMEM = STAGES * STAGE + SLOTS * SLOT + 256 + GROUP_INTS * 4 + 1024;
 constexpr uint32_t SF_COL = GN;               // TMEM columns of the scales: 4 chunks of 48
 
 struct GemmArgs {
@@ -179,9 +181,10 @@ __device__ __forceinline__ bool elect_lane() {
   return p != 0;
 }
 
-// Arrival at a barrier of the pair that hands over no memory writes (the
-// accumulator's columns, read by tcgen05.ld that has completed), so without
-// the release at cluster scope.
+// Arrival at a barrier of the pair's even CTA without a release at cluster
+// scope: no generic write is handed over to the other CTA's threads (the
+// accumulator's columns have been read by tcgen05.ld; scale atoms are read by
+// the async proxy of the CTA that wrote them, behind its proxy fence).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
@@ -211,6 +214,17 @@ __device__ __forceinline__ uint32_t fp4_idesc(int cols, uint32_t id) {
          ((FMT == KRONQ_MXFP4 ? 1u : 0u) << 23) | ((uint32_t)(GM >> 4) << 24) | (id << 29);
 }
 
+// Waits for a barrier's phase.  The first try is the common case and costs one
+// instruction; the bounded wait (which records a time-out) and the look at the
+// CTA's abort flag come only after it fails.
+__device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, volatile int* abort_s) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (*abort_s) return false;
+  if (mbar_wait(bar, parity)) return true;
+  *abort_s = 1;
+  return false;
+}
+
 // Bytes of word j of a 16-byte piece of which `valid` bytes are data.
 __device__ __forceinline__ uint32_t tail_mask(int valid, int j) {
   const int left = valid - 4 * j;
@@ -219,20 +233,20 @@ __device__ __forceinline__ uint32_t tail_mask(int valid, int j) {
 
 template <int FMT, bool BF16, bool PART>
 __global__ void __launch_bounds__(THREADS, 1)
-    fp4_gemm_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const GemmArgs a) {
-  // chunks per 16-byte scale piece and per loader step
-  constexpr int CPP = FMT == KRONQ_NVFP4 ? 1 : 2, CPS = 4 * CPP;
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
+                    const __grid_constant__ CUtensorMap mXfull, const GemmArgs a) {
+  constexpr int CPP = FMT == KRONQ_NVFP4 ? 1 : 2;   // chunks per 16-byte scale piece
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sfmem = smem + STAGES * STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sfmem + 2 * SFBUF);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sfmem + SLOTS * SLOT);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
-  const uint32_t sffull0 = empty0 + 8 * STAGES, sfempty0 = sffull0 + 16;
-  const uint32_t accfull = sfempty0 + 16, accempty = accfull + 8, done = accempty + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 7);
+  const uint32_t sffull0 = empty0 + 8 * STAGES, sfempty0 = sffull0 + 8 * SLOTS;
+  const uint32_t accfull = sfempty0 + 8 * SLOTS, accempty = accfull + 8, done = accempty + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2 * SLOTS + 3);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* bound = reinterpret_cast<int*>(sfmem + 2 * SFBUF + 256);
+  int* bound = reinterpret_cast<int*>(sfmem + SLOTS * SLOT + 256);
   int* first = bound + KRONQ_FP4_MAX_EXPERTS + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -243,8 +257,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(sffull0 + 8 * b, rank == 0 ? LOADERS + 1 : LOADERS);
+    for (int b = 0; b < SLOTS; ++b) {
+      mbar_init(sffull0 + 8 * b, 2 * LOADERS);
       mbar_init(sfempty0 + 8 * b, 1);
     }
     mbar_init(accfull, 1);
@@ -254,6 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_mbar_init();
     prefetch_tmap(&mW);
     prefetch_tmap(&mX);
+    prefetch_tmap(&mXfull);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -281,32 +296,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int rx = (int)t.t0 + (t.cols / 2) * (int)rank;
         for (int c = t.c0; c < t.c1; ++c, ++it) {
           const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
-          if (*abort_s || !mbar_wait(empty0 + 8 * s, ph ^ 1)) {
-            *abort_s = 1;
-            ok = false;
-            break;
-          }
+          ok = await(empty0 + 8 * s, ph ^ 1, abort_s);
+          if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2u * (uint32_t)(WBOX + boxes * XBOX));
           const uint32_t st = smem_u32(smem) + s * STAGE, fb = full_lead + 8 * s;
           tma_load_2d_pair(st, &mW, fb, c * (CK / 2), rw);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d_pair(st + WBOX + b * XBOX, &mX, fb, c * (CK / 2), rx + b * XROWS);
+          if (boxes == GN / NG) {
+            tma_load_2d_pair(st + WBOX, &mXfull, fb, c * (CK / 2), rx);
+          } else {
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_pair(st + WBOX + b * XBOX, &mX, fb, c * (CK / 2), rx + b * XROWS);
+          }
         }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && elect_lane()) {
-      uint32_t it = 0, cit = 0, sit = 0;   // chunks multiplied, chunks whose scales are copied, loader steps
+      uint32_t it = 0, cit = 0, git = 0;   // chunks multiplied, chunks whose scales are copied, groups
       int done_tiles = 0;
       bool ok = true, issued = false;
-      // scales of the unit's local chunk lc into TMEM; the step's buffer is
+      // scales of the unit's local chunk lc into TMEM; the group's slot is
       // free once its last copy has run
       auto copy_scales = [&](int lc, bool last) -> bool {
-        const int in = lc % CPS;
-        if (in == 0 && (*abort_s || !mbar_wait(sffull0 + 8 * (sit & 1), (sit >> 1) & 1))) return false;
+        const int in = lc % (2 * CPP);
+        const uint32_t slot = git % SLOTS;
+        if (in == 0 && !await(sffull0 + 8 * slot, (git / SLOTS) & 1, abort_s)) return false;
         tc_fence_after();
-        const uint32_t piece = smem_u32(sfmem) + (sit & 1) * SFBUF + (in / CPP) * PIECE;
+        const uint32_t piece = smem_u32(sfmem) + slot * SLOT + (in / CPP) * PIECE;
         const uint32_t sf = tmem + SF_COL + (cit & 3) * 48;
         const bool two = t.cols > GH;
 #pragma unroll
@@ -317,9 +334,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (two) copy_atom(sf + 20 + 8 * j, atom + 4096);
         }
         issued = true;
-        if (in == CPS - 1 || last) {
-          mma_commit_pair_mc(sfempty0 + 8 * (sit & 1), 0x3);
-          ++sit;
+        if (in == 2 * CPP - 1 || last) {
+          mma_commit_pair_mc(sfempty0 + 8 * slot, 0x3);
+          ++git;
         }
         ++cit;
         return true;
@@ -327,12 +344,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int u = pair; ok && walk.get(a, u, t); u += npairs, ++done_tiles) {
         const int count = t.c1 - t.c0;
         ok = copy_scales(0, count == 1);
-        if (ok && done_tiles > 0) ok = !*abort_s && mbar_wait(accempty, (done_tiles - 1) & 1);
+        if (ok && done_tiles > 0) ok = await(accempty, (done_tiles - 1) & 1, abort_s);
         tc_fence_after();
         for (int lc = 0; ok && lc < count; ++lc, ++it) {
           if (lc + 1 < count) ok = copy_scales(lc + 1, lc + 2 == count);
           const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
-          ok = ok && !*abort_s && mbar_wait(full0 + 8 * s, ph);
+          ok = ok && await(full0 + 8 * s, ph, abort_s);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sf = tmem + SF_COL + (it & 3) * 48;
@@ -349,89 +366,108 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (ok) mma_commit_pair_mc(accfull, 0x3);
       }
-      if (!ok) *abort_s = 1;
       if (issued) {
         mma_commit_pair_mc(done, 0x1);
         mbar_wait(done, 0);
       }
-    } else if (rank == 1 && elect_lane()) {
-      const uint32_t lead = cl_map(sffull0, 0);
-      uint32_t sit = 0;
-      bool ok = true;
-      for (int u = pair; ok && walk.get(a, u, t); u += npairs)
-        for (int c = t.c0; ok && c < t.c1; c += CPS, ++sit) {
-          ok = !*abort_s && mbar_wait(sffull0 + 8 * (sit & 1), (sit >> 1) & 1);
-          if (ok) mbar_arrive_cluster(lead + 8 * (sit & 1));
-        }
-      if (!ok) *abort_s = 1;
     }
     __syncwarp();
-  } else if (warp < 2 + 2 * LOADERS) {
-    const int set = (warp - 2) / LOADERS;
-    const int i = 8 * ((warp - 2) % LOADERS) + (lane & 7), p = lane >> 3;   // row modulo 32, piece of the step
-    uint32_t sit = 0;
-    bool ok = true;
-    const int64_t wlast = (int64_t)a.E * a.m - 1;
-    for (int u = pair; ok && walk.get(a, u, t); u += npairs) {
-      const int halves = (t.cols + GH - 1) / GH;
-      // rows beyond the matrices read the last one: their results are not stored
-      const int64_t rw = (int64_t)t.e * a.m + t.m0 + GH * (int64_t)rank + i;
-      for (int c = t.c0; c < t.c1; c += CPS, ++sit) {
-        if ((int)(sit & 1) != set) continue;
-        const int byte = 16 * (c / CPP + p);
-        const int valid = a.kb - byte;
-        uint4 v[12];
+  } else if (warp < 2 + LOADERS) {
+    // Two warps load the scales of the CTA's rows of W, four those of the
+    // tile's tokens.  A group is two pieces of a unit (32 bytes of a row's
+    // scales, a sector): lane (p, i) holds piece p of rows i, i + 32, i + 64
+    // and i + 96.  AHEAD groups are in flight in registers.
+    const int part = (warp - 2) >> 1;                        // W, tokens 0 - 127, tokens 128 - 255
+    const int p = lane >> 4, i = 16 * (warp & 1) + (lane & 15);
+    const uint32_t lead = cl_map(sffull0, 0);
+    const int lds = (int)a.lds;
+    int u = pair, c = 0;                                     // the walk's unit and next chunk
+    bool more = walk.get(a, u, t);
+    if (more) c = t.c0;
+    const uint8_t* base = nullptr;                           // the unit's first row
+    int last = 0;                                            // rows beyond it read it: their results are not stored
+    auto enter = [&]() {
+      if (part == 0) {
+        const int64_t r0 = (int64_t)t.e * a.m + t.m0 + GH * (int64_t)rank, rem = (int64_t)a.E * a.m - 1 - r0;
+        last = (int)min((int64_t)GH, max(rem, (int64_t)0));
+        base = a.ws + (rem < 0 ? r0 + rem : r0) * a.lds;
+      } else {
+        const int64_t r0 = t.t0 + GH * (part - 1), rem = a.T - 1 - r0;
+        last = (int)min((int64_t)GH, max(rem, (int64_t)0));
+        base = a.xs + (rem < 0 ? r0 + rem : r0) * a.lds;
+      }
+    };
+    if (more) enter();
+    uint4 v[AHEAD][4];
+    // data bytes of the lane's piece (may be below 0 or above 16); nothing to
+    // store for a part that the tile lacks; no more groups
+    constexpr int NOTHING = -(1 << 30), END = -(1 << 30) - 1;
+    int valid[AHEAD];
+    auto issue = [&](uint4 (&w)[4]) -> int {
+      if (!more) return END;
+      const int byte = 16 * (c / CPP + p);
+      int n = NOTHING;
+      if (part < 2 || t.cols > GH) {
+        n = a.kb - byte;
+        const int at = min(byte, lds - 16);
 #pragma unroll
-        for (int q = 0; q < 12; ++q) {
-          const uint8_t* row = q < 4 ? a.ws + min(rw + 32 * q, wlast) * a.lds : a.xs + min(t.t0 + i + 32 * (q - 4), a.T - 1) * a.lds;
-          v[q] = valid > 0 && (q < 8 || halves > 1) ? __ldg(reinterpret_cast<const uint4*>(row + byte))
-                                                    : make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < 4; ++q) w[q] = __ldg(reinterpret_cast<const uint4*>(base + (min(i + 32 * q, last) * lds + at)));
+      }
+      c += 2 * CPP;
+      if (c >= t.c1) {
+        u += npairs;
+        more = walk.get(a, u, t);
+        if (more) {
+          c = t.c0;
+          enter();
         }
-        if (valid > 0 && valid < 16) {
+      }
+      return n;
+    };
 #pragma unroll
-          for (int q = 0; q < 12; ++q) {
-            v[q].x &= tail_mask(valid, 0);
-            v[q].y &= tail_mask(valid, 1);
-            v[q].z &= tail_mask(valid, 2);
-            v[q].w &= tail_mask(valid, 3);
+    for (int d = 0; d < AHEAD; ++d) valid[d] = issue(v[d]);
+    uint32_t git = 0;
+    for (bool ok = true; ok;) {
+#pragma unroll
+      for (int d = 0; d < AHEAD; ++d) {
+        if (!ok) break;
+        ok = valid[d] != END;
+        if (!ok) break;
+        const uint32_t slot = git % SLOTS;
+        ok = __all_sync(0xffffffffu, await(sfempty0 + 8 * slot, ((git / SLOTS) & 1) ^ 1, abort_s));
+        if (!ok) break;
+        ++git;
+        uint4(&w)[4] = v[d];
+        if (valid[d] != NOTHING) {
+          if (valid[d] < 16) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              w[q].x &= tail_mask(valid[d], 0);
+              w[q].y &= tail_mask(valid[d], 1);
+              w[q].z &= tail_mask(valid[d], 2);
+              w[q].w &= tail_mask(valid[d], 3);
+            }
           }
+          uint4* o = reinterpret_cast<uint4*>(sfmem + slot * SLOT + p * PIECE + part * 2048 + i * 16);
+          o[0] = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
+          o[32] = make_uint4(w[0].y, w[1].y, w[2].y, w[3].y);
+          o[64] = make_uint4(w[0].z, w[1].z, w[2].z, w[3].z);
+          o[96] = make_uint4(w[0].w, w[1].w, w[2].w, w[3].w);
+          fence_proxy_async_smem();
         }
-        int good = 1;
-        if (lane == 0) good = !*abort_s && mbar_wait(sfempty0 + 8 * (sit & 1), ((sit >> 1) & 1) ^ 1) ? 1 : 0;
-        good = __shfl_sync(0xffffffffu, good, 0);
-        if (!good) {
-          if (lane == 0) *abort_s = 1;
-          ok = false;
-          break;
-        }
-        uint8_t* dst = sfmem + (sit & 1) * SFBUF + p * PIECE + i * 16;
-#pragma unroll
-        for (int g = 0; g < 3; ++g) {
-          if (g < 1 + halves) {
-            uint4* o = reinterpret_cast<uint4*>(dst + g * 2048);
-            o[0] = make_uint4(v[4 * g].x, v[4 * g + 1].x, v[4 * g + 2].x, v[4 * g + 3].x);
-            o[32] = make_uint4(v[4 * g].y, v[4 * g + 1].y, v[4 * g + 2].y, v[4 * g + 3].y);
-            o[64] = make_uint4(v[4 * g].z, v[4 * g + 1].z, v[4 * g + 2].z, v[4 * g + 3].z);
-            o[96] = make_uint4(v[4 * g].w, v[4 * g + 1].w, v[4 * g + 2].w, v[4 * g + 3].w);
-          }
-        }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(sffull0 + 8 * (sit & 1));
+        if (lane == 0) mbar_arrive_remote(lead + 8 * slot);
+        valid[d] = issue(w);
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2 - 2 * LOADERS) >> 2;
+    const int q = warp & 3, half = (warp - 2 - LOADERS) >> 2;
     const uint32_t lead = cl_map(accempty, 0);
     int done_tiles = 0;
     for (int u = pair; walk.get(a, u, t); u += npairs, ++done_tiles) {
       int good = 1;
-      if (lane == 0) good = !*abort_s && mbar_wait(accfull, done_tiles & 1) ? 1 : 0;
-      good = __shfl_sync(0xffffffffu, good, 0);
-      if (!good) {
-        if (lane == 0) *abort_s = 1;
-        break;
-      }
+      if (lane == 0) good = await(accfull, done_tiles & 1, abort_s) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, good, 0)) break;
       tc_fence_after();
       const int64_t r = t.m0 + GH * (int64_t)rank + q * 32 + lane;
       const float xg = !PART && a.xg ? *a.xg : 1.f, wg = !PART && a.wg ? a.wg[t.e] : 1.f;
@@ -504,7 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const GemmArgs);
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GemmArgs);
 
 // Most pairs of the kernel that run at once on the current device (a property
 // of the device, asked for once per kernel), 0 on error.
@@ -549,12 +585,14 @@ cudaError_t status_fetch_fp4(int* out, cudaStream_t s) {
 
 kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   const int64_t tiles_m = ceil_div(g.m, GM), tiles_t = ceil_div(g.T, GN) + (g.offsets ? g.E : 0);
+  if (g.n > (int64_t(1) << 24)) return fail(KRONQ_ERR_UNSUPPORTED, "fp4 product: row too long");
   if (tiles_m * tiles_t > (int64_t(1) << 30)) return fail(KRONQ_ERR_UNSUPPORTED, "fp4 product: more than 2^30 tiles");
-  CUtensorMap mw, mx;
+  CUtensorMap mw, mx, mxf;
   const int64_t ldc = fp4_code_row(g.n), bytes = ceil_div(g.n, 2);
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!tma_map_2d(&mw, u8, 1, g.wc, bytes, (g.offsets ? g.E : 1) * g.m, ldc, 128, GH) ||
-      !tma_map_2d(&mx, u8, 1, g.xc, bytes, g.T, ldc, 128, XROWS))
+      !tma_map_2d(&mx, u8, 1, g.xc, bytes, g.T, ldc, 128, XROWS) ||
+      !tma_map_2d(&mxf, u8, 1, g.xc, bytes, g.T, ldc, 128, GH))
     return fail(KRONQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (fp4 product)");
   GemmArgs a;
   a.xs = g.xs; a.ws = g.ws; a.xg = g.xg; a.wg = g.wg;
@@ -586,7 +624,7 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[which], mw, mx, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[which], mw, mx, mxf, a);
   count_launch();
   if (e != cudaSuccess) return cuda_fail(e, "fp4_gemm_kernel");
   return KRONQ_OK;
