@@ -47,15 +47,15 @@ constexpr int CK = 256;                       // columns per chunk: 128 bytes of
 constexpr int WBOX = GH * 128;                // 16 KB
 constexpr int XROWS = NG / 2;                 // token rows of one TMA box
 constexpr int XBOX = XROWS * 128;             // 4 KB
-constexpr int STAGES = 5;
+constexpr int STAGES = 6;
 constexpr int STAGE = WBOX + GH * 128;        // 32 KB
 constexpr int PIECE = 3 * 2048;               // 16 scale bytes of 128 + 256 rows, as atoms
-constexpr int SLOT = 2 * PIECE, SLOTS = 4;    // a loader group; groups in shared memory
-constexpr int AHEAD = 4;                      // groups in a loader's registers
+constexpr int SLOTS = 4;                      // pieces in shared memory
+constexpr int AHEAD = 4;                      // groups of two pieces in a loader's registers
 constexpr int GROUP_INTS = 2 * (KRONQ_FP4_MAX_EXPERTS + 1);
 constexpr int LOADERS = 6, EPI = 8;           // warps
 constexpr int THREADS = 32 * (2 + LOADERS + EPI);
-constexpr int SMEM = STAGES * STAGE + SLOTS * SLOT + 256 + GROUP_INTS * 4 + 1024;
+constexpr int SMEM = STAGES * STAGE + SLOTS * PIECE + 256 + GROUP_INTS * 4 + 1024;
 constexpr uint32_t SF_COL = GN;               // TMEM columns of the scales: 4 chunks of 48
 
 struct GemmArgs {
@@ -163,13 +163,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)
       : "r"(taddr));
 }
 
-// Descriptor of a 512-byte scale atom: no swizzle, 8-row groups of 16-byte rows.
-__device__ __forceinline__ uint64_t atom_desc(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) |
-         ((uint64_t)1 << 46);
-}
-__device__ __forceinline__ void copy_atom(uint32_t tcol, uint32_t saddr) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tcol), "l"(atom_desc(saddr)) : "memory");
+// A 512-byte scale atom to four TMEM columns; lo, hi: words of its descriptor.
+__device__ __forceinline__ void copy_atom(uint32_t tcol, uint32_t lo, uint32_t hi) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\ttcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(tcol),
+      "r"(lo), "r"(hi)
+      : "memory");
 }
 
 // One lane of a converged warp, in the form from which the compiler knows that
@@ -189,20 +188,23 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// D (+)= A B for the pair; alo, blo, hi: words of the operands' descriptors.
 template <int FMT>
-__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                             uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   if (FMT == KRONQ_NVFP4)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %7, 0;\n\tmov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %7, 0;\n\tmov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %4, [%5], [%6], p;\n\t}" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 
@@ -240,13 +242,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sfmem = smem + STAGES * STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sfmem + SLOTS * SLOT);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sfmem + SLOTS * PIECE);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
   const uint32_t sffull0 = empty0 + 8 * STAGES, sfempty0 = sffull0 + 8 * SLOTS;
   const uint32_t accfull = sfempty0 + 8 * SLOTS, accempty = accfull + 8, done = accempty + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2 * SLOTS + 3);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* bound = reinterpret_cast<int*>(sfmem + SLOTS * SLOT + 256);
+  int* bound = reinterpret_cast<int*>(sfmem + SLOTS * PIECE + 256);
   int* first = bound + KRONQ_FP4_MAX_EXPERTS + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -288,14 +290,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     if (elect_lane()) {
       const uint32_t full_lead = cl_map(full0, 0);
-      uint32_t it = 0;
+      uint32_t s = 0, ph = 0;
       bool ok = true;
       for (int u = pair; ok && walk.get(a, u, t); u += npairs) {
         const int rw = (int)((int64_t)t.e * a.m + t.m0) + GH * (int)rank;
         const int boxes = t.cols / NG;
         const int rx = (int)t.t0 + (t.cols / 2) * (int)rank;
-        for (int c = t.c0; c < t.c1; ++c, ++it) {
-          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
+        for (int c = t.c0; c < t.c1; ++c) {
           ok = await(empty0 + 8 * s, ph ^ 1, abort_s);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2u * (uint32_t)(WBOX + boxes * XBOX));
@@ -307,38 +308,46 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int b = 0; b < boxes; ++b)
               tma_load_2d_pair(st + WBOX + b * XBOX, &mX, fb, c * (CK / 2), rx + b * XROWS);
           }
+          if (++s == STAGES) { s = 0; ph ^= 1; }
         }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && elect_lane()) {
-      uint32_t it = 0, cit = 0, git = 0;   // chunks multiplied, chunks whose scales are copied, groups
+      // Counters advance by increments and descriptors by adding to their low
+      // words: this thread's own instructions are as long as the MMAs.
+      uint32_t s = 0, ph = 0;                 // stage of codes
+      uint32_t slot = 0, sph = 0;             // slot of scales
+      uint32_t cbuf = 0, mbuf = 0;            // TMEM buffers: next copy's, next MMAs'
       int done_tiles = 0;
       bool ok = true, issued = false;
-      // scales of the unit's local chunk lc into TMEM; the group's slot is
-      // free once its last copy has run
+      const uint32_t stage0 = smem_u32(smem) >> 4, atom0 = (smem_u32(sfmem) >> 4) | (128u >> 4 << 16);
+      constexpr uint32_t kAtomHi = (128 >> 4) | (1u << 14);                 // no swizzle, 8-row groups of 128 bytes
+      constexpr uint32_t kCodeHi = (1024 >> 4) | (1u << 14) | (2u << 29);   // 128-byte swizzle
+      // scales of the unit's local chunk lc into TMEM; a piece's slot is free
+      // once its last copy has run
       auto copy_scales = [&](int lc, bool last) -> bool {
-        const int in = lc % (2 * CPP);
-        const uint32_t slot = git % SLOTS;
-        if (in == 0 && !await(sffull0 + 8 * slot, (git / SLOTS) & 1, abort_s)) return false;
-        tc_fence_after();
-        const uint32_t piece = smem_u32(sfmem) + slot * SLOT + (in / CPP) * PIECE;
-        const uint32_t sf = tmem + SF_COL + (cit & 3) * 48;
+        const int in = lc & (CPP - 1);
+        if (in == 0) {
+          if (!await(sffull0 + 8 * slot, sph, abort_s)) return false;
+          tc_fence_after();
+        }
+        const uint32_t atom = atom0 + slot * (PIECE >> 4) + (CPP == 1 ? 0 : in * 64);
+        const uint32_t sf = tmem + SF_COL + cbuf * 48;
         const bool two = t.cols > GH;
 #pragma unroll
         for (int j = 0; j < 4 / CPP; ++j) {
-          const uint32_t atom = piece + (CPP == 1 ? j : 2 * (in & 1) + j) * 512;
-          copy_atom(sf + 4 * j, atom);
-          copy_atom(sf + 16 + 8 * j, atom + 2048);
-          if (two) copy_atom(sf + 20 + 8 * j, atom + 4096);
+          copy_atom(sf + 4 * j, atom + 32 * j, kAtomHi);
+          copy_atom(sf + 16 + 8 * j, atom + 128 + 32 * j, kAtomHi);
+          if (two) copy_atom(sf + 20 + 8 * j, atom + 256 + 32 * j, kAtomHi);
         }
         issued = true;
-        if (in == 2 * CPP - 1 || last) {
+        if (in == CPP - 1 || last) {
           mma_commit_pair_mc(sfempty0 + 8 * slot, 0x3);
-          ++git;
+          if (++slot == SLOTS) { slot = 0; sph ^= 1; }
         }
-        ++cit;
+        cbuf = (cbuf + 1) & 3;
         return true;
       };
       for (int u = pair; ok && walk.get(a, u, t); u += npairs, ++done_tiles) {
@@ -346,23 +355,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = copy_scales(0, count == 1);
         if (ok && done_tiles > 0) ok = await(accempty, (done_tiles - 1) & 1, abort_s);
         tc_fence_after();
-        for (int lc = 0; ok && lc < count; ++lc, ++it) {
+        const uint32_t idesc = fp4_idesc<FMT>(t.cols, 0);
+        for (int lc = 0; ok && lc < count; ++lc) {
           if (lc + 1 < count) ok = copy_scales(lc + 1, lc + 2 == count);
-          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1;
           ok = ok && await(full0 + 8 * s, ph, abort_s);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sf = tmem + SF_COL + (it & 3) * 48;
-          const uint32_t st = smem_u32(smem) + s * STAGE;
+          const uint32_t sf = tmem + SF_COL + mbuf * 48;
+          const uint32_t wlo = (stage0 + s * (STAGE >> 4)) | (1u << 16);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const int j = kk / CPP;
-            mma_fp4_pair<FMT>(tmem, smem_desc_sw128(st + kk * 32, 16, 1024),
-                              smem_desc_sw128(st + WBOX + kk * 32, 16, 1024),
-                              fp4_idesc<FMT>(t.cols, CPP == 1 ? 0u : 2u * (kk & 1)), sf + 4 * j, sf + 16 + 8 * j,
-                              (lc | kk) != 0 ? 1u : 0u);
+            const uint32_t id = CPP == 1 ? 0u : 2u * (kk & 1);
+            mma_fp4_pair<FMT>(tmem, wlo + 2 * kk, wlo + (WBOX >> 4) + 2 * kk, kCodeHi, idesc | (id << 4) | (id << 29),
+                              sf + 4 * j, sf + 16 + 8 * j, (lc | kk) != 0 ? 1u : 0u);
           }
           mma_commit_pair_mc(empty0 + 8 * s, 0x3);
+          mbuf = (mbuf + 1) & 3;
+          if (++s == STAGES) { s = 0; ph ^= 1; }
         }
         if (ok) mma_commit_pair_mc(accfull, 0x3);
       }
@@ -399,12 +409,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     if (more) enter();
     uint4 v[AHEAD][4];
-    // data bytes of the lane's piece (may be below 0 or above 16); nothing to
-    // store for a part that the tile lacks; no more groups
-    constexpr int NOTHING = -(1 << 30), END = -(1 << 30) - 1;
-    int valid[AHEAD];
-    auto issue = [&](uint4 (&w)[4]) -> int {
-      if (!more) return END;
+    // data bytes of the lane's piece (may be below 0 or above 16), or nothing
+    // to store for a part that the tile lacks; the group's pieces, 0 at the end
+    constexpr int NOTHING = -(1 << 30);
+    int valid[AHEAD], pieces[AHEAD];
+    auto issue = [&](uint4 (&w)[4], int& np) -> int {
+      np = 0;
+      if (!more) return NOTHING;
+      np = c + CPP < t.c1 ? 2 : 1;
       const int byte = 16 * (c / CPP + p);
       int n = NOTHING;
       if (part < 2 || t.cols > GH) {
@@ -425,39 +437,42 @@ __global__ void __launch_bounds__(THREADS, 1)
       return n;
     };
 #pragma unroll
-    for (int d = 0; d < AHEAD; ++d) valid[d] = issue(v[d]);
-    uint32_t git = 0;
+    for (int d = 0; d < AHEAD; ++d) valid[d] = issue(v[d], pieces[d]);
+    uint32_t slot = 0, sph = 0;
     for (bool ok = true; ok;) {
 #pragma unroll
       for (int d = 0; d < AHEAD; ++d) {
         if (!ok) break;
-        ok = valid[d] != END;
+        ok = pieces[d] > 0;
         if (!ok) break;
-        const uint32_t slot = git % SLOTS;
-        ok = __all_sync(0xffffffffu, await(sfempty0 + 8 * slot, ((git / SLOTS) & 1) ^ 1, abort_s));
-        if (!ok) break;
-        ++git;
         uint4(&w)[4] = v[d];
-        if (valid[d] != NOTHING) {
-          if (valid[d] < 16) {
+        const bool stores = valid[d] != NOTHING;
+        if (stores && valid[d] < 16) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              w[q].x &= tail_mask(valid[d], 0);
-              w[q].y &= tail_mask(valid[d], 1);
-              w[q].z &= tail_mask(valid[d], 2);
-              w[q].w &= tail_mask(valid[d], 3);
-            }
+          for (int q = 0; q < 4; ++q) {
+            w[q].x &= tail_mask(valid[d], 0);
+            w[q].y &= tail_mask(valid[d], 1);
+            w[q].z &= tail_mask(valid[d], 2);
+            w[q].w &= tail_mask(valid[d], 3);
           }
-          uint4* o = reinterpret_cast<uint4*>(sfmem + slot * SLOT + p * PIECE + part * 2048 + i * 16);
-          o[0] = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
-          o[32] = make_uint4(w[0].y, w[1].y, w[2].y, w[3].y);
-          o[64] = make_uint4(w[0].z, w[1].z, w[2].z, w[3].z);
-          o[96] = make_uint4(w[0].w, w[1].w, w[2].w, w[3].w);
-          fence_proxy_async_smem();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(lead + 8 * slot);
-        valid[d] = issue(w);
+        for (int k = 0; k < pieces[d]; ++k) {
+          ok = __all_sync(0xffffffffu, await(sfempty0 + 8 * slot, sph ^ 1, abort_s));
+          if (!ok) break;
+          if (stores && p == k) {
+            uint4* o = reinterpret_cast<uint4*>(sfmem + slot * PIECE + part * 2048 + i * 16);
+            o[0] = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
+            o[32] = make_uint4(w[0].y, w[1].y, w[2].y, w[3].y);
+            o[64] = make_uint4(w[0].z, w[1].z, w[2].z, w[3].z);
+            o[96] = make_uint4(w[0].w, w[1].w, w[2].w, w[3].w);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(lead + 8 * slot);
+          if (++slot == SLOTS) { slot = 0; sph ^= 1; }
+        }
+        if (!ok) break;
+        valid[d] = issue(w, pieces[d]);
       }
     }
   } else {
