@@ -16,8 +16,9 @@
 // the 4 x 4 words in registers and store 16-byte rows of four such 512-byte
 // atoms; tcgen05.cp spreads an atom over TMEM, one chunk ahead of its MMAs.
 // They work in groups of two such pieces (32 bytes of scales of a row), four
-// groups in flight in registers and four in shared memory, because a load, its
-// way to the barrier and the copy take longer than the MMAs of a few chunks.  A tile of 256 x 256
+// groups in flight in registers and two or four in shared memory, because a
+// load, its way to the barrier and the copy take longer than the MMAs of a few
+// chunks.  A tile of 256 x 256
 // leaves 256 of the 512 TMEM columns for scales; the eight epilogue warps
 // drain the accumulator into registers first and release it before they
 // store.
@@ -47,15 +48,18 @@ constexpr int CK = 256;                       // columns per chunk: 128 bytes of
 constexpr int WBOX = GH * 128;                // 16 KB
 constexpr int XROWS = NG / 2;                 // token rows of one TMA box
 constexpr int XBOX = XROWS * 128;             // 4 KB
-constexpr int STAGES = 6;
 constexpr int STAGE = WBOX + GH * 128;        // 32 KB
 constexpr int PIECE = 3 * 2048;               // 16 scale bytes of 128 + 256 rows, as atoms
-constexpr int SLOTS = 4;                      // pieces in shared memory
-constexpr int AHEAD = 4;                      // groups of two pieces in a loader's registers
+constexpr int SLOT = 2 * PIECE;               // a loader group
+constexpr int AHEAD = 4;                      // groups in a loader's registers
+// Stages of codes and slots of scales: a group is two chunks of NVFP4, whose
+// MMAs take about as long as a slot's turn, and four of MXFP4.
+constexpr int stages(int fmt) { return fmt == KRONQ_NVFP4 ? 5 : 6; }
+constexpr int slots(int fmt) { return fmt == KRONQ_NVFP4 ? 4 : 2; }
 constexpr int GROUP_INTS = 2 * (KRONQ_FP4_MAX_EXPERTS + 1);
 constexpr int LOADERS = 6, EPI = 8;           // warps
 constexpr int THREADS = 32 * (2 + LOADERS + EPI);
-constexpr int SMEM = STAGES * STAGE + SLOTS * PIECE + 256 + GROUP_INTS * 4 + 1024;
+constexpr int smem_bytes(int fmt) { return stages(fmt) * STAGE + slots(fmt) * SLOT + 256 + GROUP_INTS * 4 + 1024; }
 constexpr uint32_t SF_COL = GN;               // TMEM columns of the scales: 4 chunks of 48
 
 struct GemmArgs {
@@ -238,17 +242,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
                     const __grid_constant__ CUtensorMap mXfull, const GemmArgs a) {
   constexpr int CPP = FMT == KRONQ_NVFP4 ? 1 : 2;   // chunks per 16-byte scale piece
+  constexpr int STAGES = stages(FMT), SLOTS = slots(FMT);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sfmem = smem + STAGES * STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sfmem + SLOTS * PIECE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sfmem + SLOTS * SLOT);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
   const uint32_t sffull0 = empty0 + 8 * STAGES, sfempty0 = sffull0 + 8 * SLOTS;
   const uint32_t accfull = sfempty0 + 8 * SLOTS, accempty = accfull + 8, done = accempty + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2 * SLOTS + 3);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* bound = reinterpret_cast<int*>(sfmem + SLOTS * PIECE + 256);
+  int* bound = reinterpret_cast<int*>(sfmem + SLOTS * SLOT + 256);
   int* first = bound + KRONQ_FP4_MAX_EXPERTS + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -325,15 +330,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t stage0 = smem_u32(smem) >> 4, atom0 = (smem_u32(sfmem) >> 4) | (128u >> 4 << 16);
       constexpr uint32_t kAtomHi = (128 >> 4) | (1u << 14);                 // no swizzle, 8-row groups of 128 bytes
       constexpr uint32_t kCodeHi = (1024 >> 4) | (1u << 14) | (2u << 29);   // 128-byte swizzle
-      // scales of the unit's local chunk lc into TMEM; a piece's slot is free
+      // scales of the unit's local chunk lc into TMEM; a group's slot is free
       // once its last copy has run
       auto copy_scales = [&](int lc, bool last) -> bool {
-        const int in = lc & (CPP - 1);
+        const int in = lc & (2 * CPP - 1);
         if (in == 0) {
           if (!await(sffull0 + 8 * slot, sph, abort_s)) return false;
           tc_fence_after();
         }
-        const uint32_t atom = atom0 + slot * (PIECE >> 4) + (CPP == 1 ? 0 : in * 64);
+        const uint32_t atom = atom0 + slot * (SLOT >> 4) + (in / CPP) * (PIECE >> 4) + (CPP == 1 ? 0 : (in & 1) * 64);
         const uint32_t sf = tmem + SF_COL + cbuf * 48;
         const bool two = t.cols > GH;
 #pragma unroll
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (two) copy_atom(sf + 20 + 8 * j, atom + 256 + 32 * j, kAtomHi);
         }
         issued = true;
-        if (in == CPP - 1 || last) {
+        if (in == 2 * CPP - 1 || last) {
           mma_commit_pair_mc(sfempty0 + 8 * slot, 0x3);
           if (++slot == SLOTS) { slot = 0; sph ^= 1; }
         }
@@ -409,14 +414,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     if (more) enter();
     uint4 v[AHEAD][4];
-    // data bytes of the lane's piece (may be below 0 or above 16), or nothing
-    // to store for a part that the tile lacks; the group's pieces, 0 at the end
-    constexpr int NOTHING = -(1 << 30);
-    int valid[AHEAD], pieces[AHEAD];
-    auto issue = [&](uint4 (&w)[4], int& np) -> int {
-      np = 0;
-      if (!more) return NOTHING;
-      np = c + CPP < t.c1 ? 2 : 1;
+    // data bytes of the lane's piece (may be below 0 or above 16); nothing to
+    // store for a part that the tile lacks; no more groups
+    constexpr int NOTHING = -(1 << 30), END = NOTHING - 1;
+    int valid[AHEAD];
+    auto issue = [&](uint4 (&w)[4]) -> int {
+      if (!more) return END;
       const int byte = 16 * (c / CPP + p);
       int n = NOTHING;
       if (part < 2 || t.cols > GH) {
@@ -437,42 +440,38 @@ __global__ void __launch_bounds__(THREADS, 1)
       return n;
     };
 #pragma unroll
-    for (int d = 0; d < AHEAD; ++d) valid[d] = issue(v[d], pieces[d]);
+    for (int d = 0; d < AHEAD; ++d) valid[d] = issue(v[d]);
     uint32_t slot = 0, sph = 0;
     for (bool ok = true; ok;) {
 #pragma unroll
       for (int d = 0; d < AHEAD; ++d) {
         if (!ok) break;
-        ok = pieces[d] > 0;
+        ok = valid[d] != END;
+        if (!ok) break;
+        ok = __all_sync(0xffffffffu, await(sfempty0 + 8 * slot, sph ^ 1, abort_s));
         if (!ok) break;
         uint4(&w)[4] = v[d];
-        const bool stores = valid[d] != NOTHING;
-        if (stores && valid[d] < 16) {
+        if (valid[d] != NOTHING) {
+          if (valid[d] < 16) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            w[q].x &= tail_mask(valid[d], 0);
-            w[q].y &= tail_mask(valid[d], 1);
-            w[q].z &= tail_mask(valid[d], 2);
-            w[q].w &= tail_mask(valid[d], 3);
+            for (int q = 0; q < 4; ++q) {
+              w[q].x &= tail_mask(valid[d], 0);
+              w[q].y &= tail_mask(valid[d], 1);
+              w[q].z &= tail_mask(valid[d], 2);
+              w[q].w &= tail_mask(valid[d], 3);
+            }
           }
+          uint4* o = reinterpret_cast<uint4*>(sfmem + slot * SLOT + p * PIECE + part * 2048 + i * 16);
+          o[0] = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
+          o[32] = make_uint4(w[0].y, w[1].y, w[2].y, w[3].y);
+          o[64] = make_uint4(w[0].z, w[1].z, w[2].z, w[3].z);
+          o[96] = make_uint4(w[0].w, w[1].w, w[2].w, w[3].w);
+          fence_proxy_async_smem();
         }
-        for (int k = 0; k < pieces[d]; ++k) {
-          ok = __all_sync(0xffffffffu, await(sfempty0 + 8 * slot, sph ^ 1, abort_s));
-          if (!ok) break;
-          if (stores && p == k) {
-            uint4* o = reinterpret_cast<uint4*>(sfmem + slot * PIECE + part * 2048 + i * 16);
-            o[0] = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
-            o[32] = make_uint4(w[0].y, w[1].y, w[2].y, w[3].y);
-            o[64] = make_uint4(w[0].z, w[1].z, w[2].z, w[3].z);
-            o[96] = make_uint4(w[0].w, w[1].w, w[2].w, w[3].w);
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(lead + 8 * slot);
-          if (++slot == SLOTS) { slot = 0; sph ^= 1; }
-        }
-        if (!ok) break;
-        valid[d] = issue(w, pieces[d]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(lead + 8 * slot);
+        if (++slot == SLOTS) { slot = 0; sph ^= 1; }
+        valid[d] = issue(w);
       }
     }
   } else {
@@ -559,13 +558,13 @@ using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
 
 // Most pairs of the kernel that run at once on the current device (a property
 // of the device, asked for once per kernel), 0 on error.
-int active_pairs(Kernel fn, int which) {
+int active_pairs(Kernel fn, int which, int smem) {
   static std::atomic<int> known[64][8];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int v = known[dev][which].load(std::memory_order_relaxed);
   if (v > 0) return v;
-  if (allow_smem(reinterpret_cast<const void*>(fn), SMEM) != cudaSuccess) return 0;
+  if (allow_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -573,7 +572,7 @@ int active_pairs(Kernel fn, int which) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)(2 * (sm_count() / 2)));
@@ -624,7 +623,7 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   static const Kernel kernels[4] = {fp4_gemm_kernel<KRONQ_MXFP4, false, false>, fp4_gemm_kernel<KRONQ_MXFP4, true, false>,
                                     fp4_gemm_kernel<KRONQ_NVFP4, false, false>, fp4_gemm_kernel<KRONQ_NVFP4, true, false>};
   const int which = 2 * (fmt == KRONQ_NVFP4) + (g.y_bf16 ? 1 : 0);
-  const int pairs = active_pairs(kernels[which], which);
+  const int smem = smem_bytes(fmt), pairs = active_pairs(kernels[which], which, smem);
   if (pairs < 1) return fail(KRONQ_ERR_CUDA, "fp4 product: no pair of SMs can run the kernel");
   const int64_t most = tiles_m * tiles_t;
   cudaLaunchConfig_t cfg = {};
@@ -634,7 +633,7 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
