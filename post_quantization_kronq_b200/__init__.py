@@ -328,15 +328,18 @@ def _fp4_call(fn, device, stream, *args):
     """One library call with the tensors' device current, on the given stream or that device's current one."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device == device:
+        raw = stream.cuda_stream
+    else:
         raise ValueError(f"stream of {stream.device} for tensors on {device}")
     if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream.cuda_stream)
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
-    check(status)
+            status = fn(*args, raw)
+    if status:
+        check(status)
 
 
 def _fp4_matrix(t, name):

@@ -99,7 +99,8 @@ struct QuantArgs {
   int npartial;
   void* deq;              // dequantised values in x's type, or NULL
   int64_t ldd;
-  int vec_in, vec_out;
+  int vec_in, vec_out;      // rows are 32-byte aligned
+  uintptr_t x_lo, x_hi;     // first byte of x, one behind its last
 };
 
 // RN_e4m3(amax / (6 g)), ties to even, at most 448: the byte.
@@ -153,35 +154,132 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// 32-byte global loads and stores (whole sectors a lane).
+__device__ __forceinline__ void load32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // 16 elements of a row from column j0 (bf16: pairs in w[0..7], f32: w[0..15]);
-// columns from n on are zero.
+// columns from n on are zero.  Rows that are not 32-byte aligned are read as
+// the 16-byte words around the elements and shifted into place; the words
+// stay inside x's first to last element, next to which single elements are
+// read instead.
 template <bool BF16>
 __device__ __forceinline__ void load16(const QuantArgs& a, int64_t r, int64_t j0, uint32_t (&w)[BF16 ? 8 : 16]) {
   constexpr int NW = BF16 ? 8 : 16;
   const char* p = static_cast<const char*>(a.x) + (r * a.ldx + j0) * (BF16 ? 2 : 4);
   if (a.vec_in && j0 + 16 <= a.n) {
+    load32(p, w);
+    if (!BF16) load32(p + 32, w + (BF16 ? 0 : 8));
+    return;
+  }
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+  if (j0 + 16 <= a.n && lo >= a.x_lo && lo + NW * 4 + 16 <= a.x_hi) {
+    uint32_t c[NW + 4];
 #pragma unroll
-    for (int q = 0; q < NW / 4; ++q) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[q];
-      w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+    for (int q = 0; q < NW / 4 + 1; ++q) {
+      const uint4 v = reinterpret_cast<const uint4*>(lo)[q];
+      c[4 * q] = v.x; c[4 * q + 1] = v.y; c[4 * q + 2] = v.z; c[4 * q + 3] = v.w;
     }
-  } else {
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    if (off & 8) {
 #pragma unroll
-    for (int q = 0; q < NW; ++q) {
-      if (BF16) {
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-        const uint32_t lo = j0 + 2 * q < a.n ? h[2 * q] : 0u;
-        const uint32_t hi = j0 + 2 * q + 1 < a.n ? h[2 * q + 1] : 0u;
-        w[q] = lo | (hi << 16);
-      } else {
-        w[q] = j0 + q < a.n ? reinterpret_cast<const uint32_t*>(p)[q] : 0u;
-      }
+      for (int q = 0; q < NW + 2; ++q) c[q] = c[q + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+      for (int q = 0; q < NW + 1; ++q) c[q] = c[q + 1];
+    }
+#pragma unroll
+    for (int q = 0; q < NW; ++q) w[q] = BF16 ? __funnelshift_r(c[q], c[q + 1], 8 * (off & 2)) : c[q];
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < NW; ++q) {
+    if (BF16) {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+      const uint32_t e0 = j0 + 2 * q < a.n ? h[2 * q] : 0u;
+      const uint32_t e1 = j0 + 2 * q + 1 < a.n ? h[2 * q + 1] : 0u;
+      w[q] = e0 | (e1 << 16);
+    } else {
+      w[q] = j0 + q < a.n ? reinterpret_cast<const uint32_t*>(p)[q] : 0u;
+    }
+  }
+}
+
+// A warp's 32 runs of up to 16 values, each to its place in a row: `at` the
+// element offset, `count` the elements (0 for a lane without any).  Aligned
+// rows take 32-byte stores.  Others go through shared memory, so that a store
+// instruction writes two runs' neighbouring elements, not one of each lane's.
+struct RunSmem {
+  float v[32 * 17];
+  int64_t at[32];
+  int count[32];
+};
+template <bool BF16>
+__device__ __forceinline__ void store_runs(void* out, int64_t at, int count, bool vec, const float (&v)[16], RunSmem& sm,
+                                           int lane) {
+  const bool whole = vec && count == 16;
+  if (whole) {
+    if (BF16) {
+      uint32_t u[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) u[q] = as_u32(__floats2bfloat162_rn(v[2 * q], v[2 * q + 1]));
+      store32(static_cast<__nv_bfloat16*>(out) + at, u);
+    } else {
+      uint32_t u[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(v[q]);
+      store32(static_cast<float*>(out) + at, u);
+      store32(static_cast<float*>(out) + at + 8, u + 8);
+    }
+  }
+  if (__all_sync(0xffffffffu, whole || count == 0)) return;
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 16; ++q) sm.v[lane * 17 + q] = v[q];
+  sm.at[lane] = at;
+  sm.count[lane] = whole ? 0 : count;
+  __syncwarp();
+  const int e = lane & 15;
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    const int u = 2 * k + (lane >> 4);
+    if (e < sm.count[u]) {
+      const float f = sm.v[u * 17 + e];
+      if (BF16) static_cast<__nv_bfloat16*>(out)[sm.at[u] + e] = __float2bfloat16_rn(f);
+      else static_cast<float*>(out)[sm.at[u] + e] = f;
+    }
+  }
+  __syncwarp();
+}
+
+// Values of 16 codes under a scale (and the tensor scale), with float32's roundings.
+template <int FMT>
+__device__ __forceinline__ void values16(uint32_t lo, uint32_t hi, float s, float g, float (&v)[16]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float2 d = e2m1x2_float2(((q < 4 ? lo : hi) >> (8 * (q & 3))) & 0xFFu);
+    v[2 * q] = __fmul_rn(d.x, s);
+    v[2 * q + 1] = __fmul_rn(d.y, s);
+    if (FMT == KRONQ_NVFP4) {
+      v[2 * q] = __fmul_rn(v[2 * q], g);
+      v[2 * q + 1] = __fmul_rn(v[2 * q + 1], g);
     }
   }
 }
 
 template <int FMT, bool BF16>
 __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) {
+  __shared__ RunSmem runs[QT / 32];
   float g = 1.f;
   bool g_bad = false;
   if (FMT == KRONQ_NVFP4) {
@@ -305,45 +403,12 @@ __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) 
       if (j0 + 16 > a.n && j0 < a.n)   // the sign of a padding zero is +
         packed &= (1ull << (4 * (a.n - j0))) - 1ull;
       if (c * 8 < a.ldc) *reinterpret_cast<uint64_t*>(a.codes + r * a.ldc + c * 8) = packed;
-      if (a.deq && j0 < a.n) {
-        const float s = fp4_scale_value<FMT>(sbyte);
-        float v[16];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float2 d = e2m1x2_float2((uint32_t)(packed >> (8 * q)) & 0xFFu);
-          v[2 * q] = __fmul_rn(d.x, s);
-          v[2 * q + 1] = __fmul_rn(d.y, s);
-          if (FMT == KRONQ_NVFP4) {
-            v[2 * q] = __fmul_rn(v[2 * q], g);
-            v[2 * q + 1] = __fmul_rn(v[2 * q + 1], g);
-          }
-        }
-        if (BF16) {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.deq) + r * a.ldd + j0;
-          if (a.vec_out && j0 + 16 <= a.n) {
-            uint32_t u[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) u[q] = as_u32(__floats2bfloat162_rn(v[2 * q], v[2 * q + 1]));
-            reinterpret_cast<uint4*>(o)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-            reinterpret_cast<uint4*>(o)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-              if (j0 + q < a.n) o[q] = __float2bfloat16_rn(v[q]);
-          }
-        } else {
-          float* o = static_cast<float*>(a.deq) + r * a.ldd + j0;
-          if (a.vec_out && j0 + 16 <= a.n) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              reinterpret_cast<float4*>(o)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-              if (j0 + q < a.n) o[q] = v[q];
-          }
-        }
-      }
+    }
+    if (a.deq) {
+      float v[16];
+      values16<FMT>((uint32_t)packed, (uint32_t)(packed >> 32), fp4_scale_value<FMT>(sbyte), g, v);
+      const int count = live && j0 < a.n ? (int)min((int64_t)16, a.n - j0) : 0;
+      store_runs<BF16>(a.deq, r * a.ldd + j0, count, a.vec_out, v, runs[threadIdx.x >> 5], threadIdx.x & 31);
     }
     i += stride;
     r += dr;
@@ -363,54 +428,48 @@ struct DequantArgs {
   int vec_out;
 };
 
+// Each warp step takes UNROLL runs of 16 codes a lane, so that enough loads
+// are in flight: a run reads only 9 bytes for the 32 or 64 that it writes.
+constexpr int UNROLL = 4;
+
 template <int FMT, bool BF16>
 __global__ void __launch_bounds__(QT) fp4_dequantize_kernel(const DequantArgs a) {
+  __shared__ RunSmem runs[QT / 32];
   const float g = FMT == KRONQ_NVFP4 ? *a.gscale : 1.f;
   const int64_t per = (a.n + 15) / 16;
   const int64_t total = a.rows * per;
-  const int64_t stride = (int64_t)gridDim.x * QT;
-  int64_t i = (int64_t)blockIdx.x * QT + threadIdx.x;
-  int64_t r = i / per, c = i - r * per;
-  const int64_t dr = stride / per, dc = stride - dr * per;
-  for (; i < total; i += stride) {
-    const int64_t j0 = c * 16;
-    const uint2 w = *reinterpret_cast<const uint2*>(a.codes + r * a.ldc + c * 8);
-    const float s = fp4_scale_value<FMT>(a.scales[r * a.lds + (FMT == KRONQ_MXFP4 ? (c >> 1) : c)]);
-    float v[16];
+  const int lane = threadIdx.x & 31;
+  const int64_t stride = (int64_t)gridDim.x * QT * UNROLL;
+  const int64_t dr = stride / per, dc = stride - dr * per;   // a step of the grid
+  int64_t base = (int64_t)blockIdx.x * QT * UNROLL + (int64_t)(threadIdx.x >> 5) * 32 * UNROLL;
+  int64_t r = (base + lane) / per, c = base + lane - r * per;
+  const int64_t ur = 32 / per, uc = 32 - ur * per;           // from run to run
+  for (; base < total; base += stride) {
+    uint2 w[UNROLL];
+    uint32_t sb[UNROLL];
+    int64_t at[UNROLL];
+    int count[UNROLL];
+    int64_t rr = r, cc = c;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float2 d = e2m1x2_float2(((q < 4 ? w.x : w.y) >> (8 * (q & 3))) & 0xFFu);
-      v[2 * q] = __fmul_rn(d.x, s);
-      v[2 * q + 1] = __fmul_rn(d.y, s);
-      if (FMT == KRONQ_NVFP4) {
-        v[2 * q] = __fmul_rn(v[2 * q], g);
-        v[2 * q + 1] = __fmul_rn(v[2 * q + 1], g);
+    for (int k = 0; k < UNROLL; ++k) {
+      const bool live = base + 32 * k + lane < total;
+      w[k] = make_uint2(0, 0);
+      sb[k] = 0;
+      if (live) {
+        w[k] = *reinterpret_cast<const uint2*>(a.codes + rr * a.ldc + cc * 8);
+        sb[k] = a.scales[rr * a.lds + (FMT == KRONQ_MXFP4 ? (cc >> 1) : cc)];
       }
+      at[k] = rr * a.ldo + cc * 16;
+      count[k] = live ? (int)min((int64_t)16, a.n - cc * 16) : 0;
+      rr += ur;
+      cc += uc;
+      if (cc >= per) { cc -= per; ++rr; }
     }
-    if (BF16) {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + r * a.ldo + j0;
-      if (a.vec_out && j0 + 16 <= a.n) {
-        uint32_t u[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) u[q] = as_u32(__floats2bfloat162_rn(v[2 * q], v[2 * q + 1]));
-        reinterpret_cast<uint4*>(o)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        reinterpret_cast<uint4*>(o)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          if (j0 + q < a.n) o[q] = __float2bfloat16_rn(v[q]);
-      }
-    } else {
-      float* o = static_cast<float*>(a.out) + r * a.ldo + j0;
-      if (a.vec_out && j0 + 16 <= a.n) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          reinterpret_cast<float4*>(o)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          if (j0 + q < a.n) o[q] = v[q];
-      }
+    for (int k = 0; k < UNROLL; ++k) {
+      float v[16];
+      values16<FMT>(w[k].x, w[k].y, fp4_scale_value<FMT>(sb[k]), g, v);
+      store_runs<BF16>(a.out, at[k], count[k], a.vec_out, v, runs[threadIdx.x >> 5], lane);
     }
     r += dr;
     c += dc;
@@ -418,9 +477,10 @@ __global__ void __launch_bounds__(QT) fp4_dequantize_kernel(const DequantArgs a)
   }
 }
 
-// Blocks for `total` units of one thread each: whole waves of 8 per SM.
-unsigned quant_grid(int64_t total) {
-  const int64_t want = ceil_div(total, QT), cap = 8 * (int64_t)sm_count();
+// Blocks for `total` units of one thread each: at most as many as run at once
+// (per_sm: the kernel's registers allow that many).
+unsigned quant_grid(int64_t total, int per_sm) {
+  const int64_t want = ceil_div(total, QT), cap = per_sm * (int64_t)sm_count();
   return (unsigned)(want < 1 ? 1 : want < cap ? want : cap);
 }
 
@@ -472,14 +532,16 @@ kronq_status kronq_fp4_quantize(const void* x, kronq_dtype dt, int64_t rows, int
   a.gscale = gscale;
   a.partial = nullptr; a.npartial = 0;
   a.deq = deq; a.ldd = ldd;
-  a.vec_in = aligned(x, 16) && (ldx * esize) % 16 == 0;
-  a.vec_out = deq && aligned(deq, 16) && (ldd * esize) % 16 == 0;
+  a.vec_in = aligned(x, 32) && (ldx * esize) % 32 == 0;
+  a.vec_out = deq && aligned(deq, 32) && (ldd * esize) % 32 == 0;
+  a.x_lo = reinterpret_cast<uintptr_t>(x);
+  a.x_hi = a.x_lo + (size_t)(rows > 0 ? (rows - 1) * ldx + n : 0) * esize;
   if (compute) {
     uint32_t* partial = rows > 0 ? static_cast<uint32_t*>(workspace) : reinterpret_cast<uint32_t*>(gscale);
     a.partial = partial;
     if (rows > 0) {
       const int64_t units = rows * (a.vec_in ? ceil_div(n, 16 / esize) : n);
-      unsigned grid = quant_grid(ceil_div(units, 4));   // four loads in flight a thread
+      unsigned grid = quant_grid(ceil_div(units, 4), 6);   // four loads in flight a thread
       if (grid > (unsigned)MAX_PARTIALS) grid = MAX_PARTIALS;
       if (dt == KRONQ_BF16) fp4_amax_kernel<true><<<grid, QT, 0, st>>>(x, rows, n, ldx, a.vec_in, partial);
       else fp4_amax_kernel<false><<<grid, QT, 0, st>>>(x, rows, n, ldx, a.vec_in, partial);
@@ -487,7 +549,7 @@ kronq_status kronq_fp4_quantize(const void* x, kronq_dtype dt, int64_t rows, int
       a.npartial = (int)grid;
     }
   }
-  const unsigned grid = quant_grid(rows * a.lds * (fmt == KRONQ_MXFP4 ? 2 : 1));
+  const unsigned grid = quant_grid(rows * a.lds * (fmt == KRONQ_MXFP4 ? 2 : 1), 4);
   if (fmt == KRONQ_MXFP4) {
     if (dt == KRONQ_BF16) fp4_quantize_kernel<KRONQ_MXFP4, true><<<grid, QT, 0, st>>>(a);
     else fp4_quantize_kernel<KRONQ_MXFP4, false><<<grid, QT, 0, st>>>(a);
@@ -518,8 +580,8 @@ kronq_status kronq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, c
   a.codes = codes; a.scales = scales; a.rows = rows; a.n = n;
   a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
   a.gscale = gscale; a.out = out; a.ldo = ldo;
-  a.vec_out = aligned(out, 16) && (ldo * esize) % 16 == 0;
-  const unsigned grid = quant_grid(rows * ceil_div(n, 16));
+  a.vec_out = aligned(out, 32) && (ldo * esize) % 32 == 0;
+  const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), UNROLL), 3);
   cudaStream_t st = as_stream(s);
   if (fmt == KRONQ_MXFP4) {
     if (dt == KRONQ_BF16) fp4_dequantize_kernel<KRONQ_MXFP4, true><<<grid, QT, 0, st>>>(a);
