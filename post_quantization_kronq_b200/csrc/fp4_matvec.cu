@@ -3,26 +3,29 @@
 //
 // Bound by HBM: each weight is 4 bits plus its share of a scale and is used
 // once per token.  A CTA of eight warps owns 16 rows at a time, the warps
-// split the columns in interleaved spans of 128 (lane t of a row's four loads
-// 16 bytes of codes, 32 weights), four spans in flight ahead of the
-// arithmetic.  The products run on mma.sync (m16n8k16, bf16 in, float32
-// out), rows on the M side, tokens on the N side: one weight load serves 8
-// tokens at the price of one.
+// split the columns in interleaved spans of 128 (lane t of a row's four takes
+// 16 bytes of codes, 32 weights).  Each warp copies its spans into a ring of
+// its own in shared memory with cp.async, RING spans ahead and on into the
+// next rows: loads into registers this far ahead share the warp's few
+// scoreboards, and a wait for the first became one for the last.  The products run on mma.sync (m16n8k16, fp16 in, float32 out),
+// rows on the M side, tokens on the N side: one weight load serves 8 tokens
+// at the price of one.
 //
-// Weights in bf16 are exact.  A code's bits seem, shifted to the sign and the
-// lowest exponent and highest mantissa bits of bf16, are the value times
-// 2^-126 (0.5 as a subnormal); one multiplication by scale * 2^118 gives
-// value * scale * 2^-8, at most 6 significant bits.  The sums carry 2^-8 to
-// their end.  An E8M0 scale outside 2^-119 .. 2^9 takes a second
-// multiplication instead.  float32 tokens are three bf16 parts of 8 bits,
-// the second and third scaled by 2^8 and 2^16 against underflow, with a sum
-// each: all 24 bits take part.
+// Both operands are exact in fp16, or nearly so.  A weight is E2M1 times its
+// block scale, at most 6 significant bits: one conversion and one
+// multiplication for two weights (E8M0 scales are taken times 2^12, good for
+// 2^-35 .. 2^1).  A token's span of 128 columns is scaled by a power of two
+// that brings its largest magnitude to [2^14, 2^15): bf16 values down to
+// 2^-31 of it are exact; a float32 value is two parts of 11 bits (2^-23 off
+// at most) down to 2^-28 of it.  The sum over a span is scaled back when it
+// joins the float32 sum of the row.  Spans that this does not cover (a wider
+// range within 128 columns, infinities and NaN, E8M0 scales beyond the range)
+// are computed in float32, one weight and token at a time.
 //
 // The order of k inside an mma is free as long as weights and tokens agree:
-// lane t of a span holds k = 32 t + 8 j + {0..7} as word j, whose pairs
-// (i, i + 4) are the halves of one register.  Tokens are staged in shared
-// memory in that order, 16-byte pieces placed so that a warp reads without
-// bank conflicts.
+// lane t of a span holds k = 32 t + 8 j + {0..7} as word j.  Tokens are staged
+// in shared memory in that order, 16-byte pieces placed so that a warp reads
+// without bank conflicts.
 #include <algorithm>
 
 #include "fp4.cuh"
@@ -34,8 +37,11 @@ namespace {
 
 constexpr int VT = 256, VW = VT / 32;
 constexpr int SPAN = 128;                 // columns of one step of a warp
-constexpr int BATCH = 4;                  // steps in flight
-constexpr int XSMEM = 80 * 1024;          // most shared memory for tokens: two CTAs on an SM
+constexpr int PAIR = 2;                   // spans of a step: two independent chains of mma
+constexpr int RING = 3;                   // steps of a warp in shared memory
+constexpr int RSLOT = 16 * SPAN / 2 + 16 * 8;   // codes of 16 rows, up to 8 scale bytes of each
+constexpr int RBYTES = VW * RING * PAIR * RSLOT;
+constexpr int XSMEM = 40 * 1024;          // most shared memory for tokens: two CTAs on an SM
 
 struct VecArgs {
   const void* x;
@@ -46,260 +52,357 @@ struct VecArgs {
   int64_t m, n, ldc, lds;
   int kslice;             // columns of a slice, a multiple of SPAN (grid.y slices)
   int xrow;               // bytes of a token's part in shared memory
-  int vec;                // 16-byte loads of x
+  int vec;                // 4-element loads of x
   void* y;
   int y_bf16;
   int64_t ldy;
-  float* part;            // partial sums [slice][T][m] (times 2^-8), or NULL
+  float* part;            // partial sums [slice][T][m], or NULL
 };
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-
-// Codes i and i + 4 of a word as bf16 halves, times 2^-126.
-template <int I>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  constexpr int up = 12 - 4 * I, mag = 6 - 4 * I;
-  const uint32_t s = (up ? w << up : w) & 0x80008000u;
-  const uint32_t e = (mag >= 0 ? w << (mag >= 0 ? mag : 0) : w >> (mag < 0 ? -mag : 0)) & 0x01C001C0u;
-  return s | e;
+// The eight codes of a word as four pairs of halves, in order.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ float x_at(const VecArgs& a, bool f32, int64_t at) {
+  return f32 ? static_cast<const float*>(a.x)[at]
+             : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.x)[at] << 16);
 }
 
-// Twice in a word: bf16 of an E4M3 scale times 2^118, of an E8M0 one times
-// 2^118 (wide: times 2^-8 for the second multiplication by 2^126).
-__device__ __forceinline__ uint32_t dup_bf16(float f) {
-  const uint32_t u = __float_as_uint(f) >> 16;   // exact: at most 4 significant bits (NaN keeps its top bits)
-  return u | (u << 16);
-}
+// E8M0 scales that the fp16 path takes, and their power of two.
+constexpr uint32_t kMxLow = 127 - 35, kMxHigh = 127 + 1;
+constexpr int kMxShift = 12;
 
 template <int FMT, bool XF32, int NT>
 struct Vec {
-  static constexpr int PARTS = XF32 ? 3 : 1;
+  static constexpr int PARTS = XF32 ? 2 : 1;
   static constexpr int BPL = FMT == KRONQ_NVFP4 ? 2 : 1;   // scale blocks of a lane's 32 columns
 
   struct Load {
     uint4 w[2];
     uint32_t s[2];
   };
-
-  // Span `sp` of rows r0 + g and r0 + g + 8: codes beyond the row read as
-  // zeros, scales beyond it are masked in use.
-  static __device__ __forceinline__ void load(const VecArgs& a, int64_t r0, int64_t k, int g, Load& v) {
+  // What a lane copies of a tile: 16 bytes of codes of rows g and g + 8, and
+  // four scale bytes of one row (NVFP4: lane / 2, MXFP4: lane, of the first 16).
+  struct Rows {
+    const uint8_t *c[2], *s;
+  };
+  static __device__ __forceinline__ Rows rows(const VecArgs& a, int64_t tile, int64_t k0, int lane) {
+    Rows p;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)   // rows beyond m read the last one: their results are not stored
+      p.c[h] = a.wc + min(tile * 16 + (lane >> 2) + 8 * h, a.m - 1) * a.ldc + (k0 >> 1) + 16 * (lane & 3);
+    const int row = BPL == 2 ? lane >> 1 : lane & 15;
+    p.s = a.ws + min(tile * 16 + row, a.m - 1) * a.lds + k0 / (32 / BPL) + (BPL == 2 ? 4 * (lane & 1) : 0);
+    return p;
+  }
+  // Span sp into a ring slot, zeros where it is not there (`there`) or the
+  // lane's codes do not lie within the row (`inside`).
+  static __device__ __forceinline__ void copy(const Rows& p, int sp, bool there, bool inside, uint32_t slot, int lane) {
+    const int n = there && inside ? 16 : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + 512 * h + 16 * lane),
+                   "l"(p.c[h] + (n ? sp * (SPAN / 2) : 0)), "r"(n)
+                   : "memory");
+    if (BPL == 2 || lane < 16)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot + 1024 + 4 * lane),
+                   "l"(p.s + (there ? sp * (4 * BPL) : 0)), "r"(there ? 4 : 0)
+                   : "memory");
+  }
+  static __device__ __forceinline__ Load take(const uint8_t* slot, int lane) {
+    Load v;
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t r = min(r0 + g + 8 * h, a.m - 1);
-      if ((k >> 1) < a.ldc) {
-        v.w[h] = __ldcs(reinterpret_cast<const uint4*>(a.wc + r * a.ldc + (k >> 1)));
-        const uint8_t* s = a.ws + r * a.lds + k / (32 / BPL);
-        v.s[h] = BPL == 2 ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(s)) : (uint32_t)__ldg(s);
-      } else {
-        v.w[h] = make_uint4(0, 0, 0, 0);
-        v.s[h] = 0;
-      }
+      v.w[h] = *reinterpret_cast<const uint4*>(slot + 512 * h + 16 * lane);
+      const uint8_t* s = slot + 1024 + (g + 8 * h) * (4 * BPL) + t * BPL;
+      v.s[h] = BPL == 2 ? (uint32_t)*reinterpret_cast<const uint16_t*>(s) : (uint32_t)*s;
     }
+    return v;
   }
 
-  static __device__ __forceinline__ void word(const uint32_t (&w)[2], const uint32_t (&mul)[2], bool wide,
-                                              const uint4 (&x)[NT][PARTS], float (&acc)[NT][PARTS][4]) {
-    uint32_t p[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      p[h][0] = code_pair<0>(w[h]);
-      p[h][1] = code_pair<1>(w[h]);
-      p[h][2] = code_pair<2>(w[h]);
-      p[h][3] = code_pair<3>(w[h]);
-      if (FMT == KRONQ_MXFP4 && wide) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[h][i] = mul_bf16x2(p[h][i], 0x7E807E80u);   // 2^126
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[h][i] = mul_bf16x2(p[h][i], mul[h]);
-    }
-    // registers: rows g, g + 8 at the first k pair, then at the second
-    const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
-    const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        mma_16816(acc[nt][q], a0, x[nt][q].x, x[nt][q].y);
-        mma_16816(acc[nt][q], a1, x[nt][q].z, x[nt][q].w);
-      }
-  }
-
-  static __device__ __forceinline__ void step(const VecArgs& a, const Load& v, int64_t k, const uint8_t* xs, int g,
-                                              float (&acc)[NT][PARTS][4]) {
-    // multipliers of the lane's blocks; blocks at or beyond n count as zero
-    uint32_t mul[2][BPL];
-    bool wide = false;
+  // Multipliers of the lane's blocks (its columns begin at k; those from kend
+  // on count as zero); true where one is beyond what fp16 takes.
+  static __device__ __forceinline__ bool multipliers(const Load& v, int64_t k, int64_t kend, uint32_t (&mul)[2][BPL]) {
+    bool odd = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (FMT == KRONQ_NVFP4) {
-#pragma unroll
-        for (int b = 0; b < BPL; ++b) {
-          const uint32_t byte = k + 16 * b < a.n ? (v.s[h] >> (8 * b)) & 0xFFu : 0u;
-          mul[h][b] = dup_bf16(e4m3_value(byte) * 0x1p118f);
-        }
+        uint32_t two = v.s[h], f;
+        if (k + 32 > kend) two = k >= kend ? 0u : k + 16 >= kend ? two & 0xFFu : two;
+        asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(f) : "r"(two));
+        mul[h][0] = __byte_perm(f, f, 0x1010);
+        mul[h][BPL - 1] = __byte_perm(f, f, 0x3232);
       } else {
-        const bool in = k < a.n;
-        wide |= in && (v.s[h] < 8u || v.s[h] > 136u);
-        mul[h][0] = in ? dup_bf16(__uint_as_float((v.s[h] + 118u) << 23)) : 0u;
+        const bool in = k < kend;
+        odd |= in && (v.s[h] < kMxLow || v.s[h] > kMxHigh);
+        // fp16 2^(byte - 127 + 12), subnormal below 2^-14
+        const int e = (int)v.s[h] - 127 + kMxShift + 15;
+        const uint32_t one = e >= 1 ? (uint32_t)e << 10 : 1024u >> (1 - e);
+        mul[h][0] = in ? one | (one << 16) : 0u;
       }
     }
-    if (FMT == KRONQ_MXFP4) {
-      wide = __any_sync(0xffffffffu, wide);
-      if (wide) {   // plain scales, the sums without their 2^-8
+    return odd;
+  }
+
+  // acc += the products of a step's spans; k: the lane's first column of the
+  // first span; xs: its first piece of the tokens there (row stride of a token
+  // and part a.xrow); fac: the factors of the lane's two tokens there; xnext,
+  // fnext: offsets of the second span's.
+  static __device__ __forceinline__ void step(const VecArgs& a, const Load (&v)[PAIR], int64_t k, int64_t kend,
+                                              const uint8_t* const (&xs)[NT], int xnext, const float* fac, int fnext,
+                                              bool plain, int lane, float (&acc)[NT][4]) {
+    uint32_t mul[PAIR][2][BPL];
+    bool odd = plain;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) mul[h][0] = k < a.n ? dup_bf16(e8m0_value(v.s[h])) : 0u;
+    for (int s = 0; s < PAIR; ++s) odd |= multipliers(v[s], k + s * SPAN, kend, mul[s]);
+    if (FMT == KRONQ_MXFP4 ? __any_sync(0xffffffffu, odd) : plain) {
+#pragma unroll
+      for (int s = 0; s < PAIR; ++s) scalar(a, v[s], k + s * SPAN, kend, lane, acc);
+      return;
+    }
+    float sum[PAIR][NT][PARTS][4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int s = 0; s < PAIR; ++s) {
+        uint32_t p[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          codes_f16(j == 0 ? v[s].w[h].x : j == 1 ? v[s].w[h].y : j == 2 ? v[s].w[h].z : v[s].w[h].w, p[h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[h][i] = mul_f16x2(p[h][i], mul[s][h][BPL == 2 ? j >> 1 : 0]);
+        }
+        // registers: rows g, g + 8 at the first k pair, then at the second
+        const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+        const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][q][e] *= 256.f;
+          for (int q = 0; q < PARTS; ++q) {
+            const uint4 x = *reinterpret_cast<const uint4*>(xs[nt] + s * xnext + q * a.xrow + j * 64);
+            mma_16816(sum[s][nt][q], a0, x.x, x.y);
+            mma_16816(sum[s][nt][q], a1, x.z, x.w);
+          }
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint4 x[NT][PARTS];
+    for (int s = 0; s < PAIR; ++s)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 f = *reinterpret_cast<const float2*>(fac + s * fnext + 8 * nt);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float w = sum[s][nt][0][e];
+          if (XF32) w = fmaf(sum[s][nt][PARTS - 1][e], 0x1p-11f, w);
+          acc[nt][e] = fmaf(w, (e & 1) ? f.y : f.x, acc[nt][e]);
+        }
+      }
+  }
+
+  // The same sums in float32 from the tokens as given.
+  static __device__ __forceinline__ void scalar(const VecArgs& a, const Load& v, int64_t k, int64_t kend, int lane, float (&acc)[NT][4]) {
+    const int t = lane & 3;
+#pragma unroll 1
+    for (int tk = 0; tk < a.T; ++tk) {
+      float s[2] = {0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {v.w[h].x, v.w[h].y, v.w[h].z, v.w[h].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t b = BPL == 2 ? (v.s[h] >> (8 * (j >> 1))) & 0xFFu : v.s[h];
+          const float sc = fp4_scale_value<FMT>(b);
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const float2 d = e2m1x2_float2((w[j] >> (8 * i)) & 0xFFu);
+            const int64_t at = k + 8 * j + 2 * i;
+            if (at < kend) s[h] = fmaf(d.x * sc, x_at(a, XF32, tk * a.ldx + at), s[h]);
+            if (at + 1 < kend) s[h] = fmaf(d.y * sc, x_at(a, XF32, tk * a.ldx + at + 1), s[h]);
+          }
+        }
+        s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
+        s[h] += __shfl_xor_sync(0xffffffffu, s[h], 2);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-          x[nt][q] = 8 * nt + g < a.T
-                         ? *reinterpret_cast<const uint4*>(xs + ((8 * nt + g) * PARTS + q) * a.xrow + j * 64)
-                         : make_uint4(0, 0, 0, 0);
-      const uint32_t w[2] = {j == 0 ? v.w[0].x : j == 1 ? v.w[0].y : j == 2 ? v.w[0].z : v.w[0].w,
-                             j == 0 ? v.w[1].x : j == 1 ? v.w[1].y : j == 2 ? v.w[1].z : v.w[1].w};
-      const uint32_t mj[2] = {mul[0][BPL == 2 ? j >> 1 : 0], mul[1][BPL == 2 ? j >> 1 : 0]};
-      word(w, mj, wide, x, acc);
-    }
-    if (FMT == KRONQ_MXFP4 && wide) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][q][e] *= 0x1p-8f;
+        if (nt == (tk >> 3) && t == ((tk & 7) >> 1)) {
+          acc[nt][0] += (tk & 1) ? 0.f : s[0];
+          acc[nt][1] += (tk & 1) ? s[0] : 0.f;
+          acc[nt][2] += (tk & 1) ? 0.f : s[1];
+          acc[nt][3] += (tk & 1) ? s[1] : 0.f;
+        }
     }
   }
 };
 
-// Byte offset of the eight columns from k on (of a slice) in a token's row:
-// spans of 256 bytes, piece j of lane t at 64 j + 16 t.
+// Byte offset of column k (of a slice) in a token's row: spans of 256 bytes,
+// piece j of lane t at 64 j + 16 t.
 __device__ __forceinline__ int x_offset(int k) {
   const int t = (k >> 5) & 3, j = (k >> 3) & 3;
-  return (k / SPAN) * 256 + j * 64 + t * 16;
+  return (k / SPAN) * 256 + j * 64 + t * 16 + (k & 7) * 2;
 }
 
 template <int FMT, bool XF32, int NT>
 __global__ void __launch_bounds__(VT, 2) fp4_matvec_kernel(const VecArgs a) {
   using V = Vec<FMT, XF32, NT>;
-  extern __shared__ __align__(16) uint8_t xs[];
+  // the warps' rings, the tokens' parts, then per span the factors of 8 NT
+  // tokens and whether the span is computed in float32
+  extern __shared__ __align__(16) uint8_t xsm[];
   __shared__ float red[2][VW][16 * 8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t k0 = (int64_t)blockIdx.y * a.kslice;
   const int cols = (int)min((int64_t)a.kslice, a.n - k0);
   const int spans = (cols + SPAN - 1) / SPAN;
-  const int nb = (spans + VW * BATCH - 1) / (VW * BATCH);   // batches of a row tile
+  const int steps = (spans + PAIR * VW - 1) / (PAIR * VW);  // of a warp for a row tile
   const int64_t tiles = (a.m + 15) / 16;
+  uint8_t* ring = xsm + warp * (RING * PAIR * RSLOT);
+  uint8_t* xpart = xsm + RBYTES;
+  float* fac = reinterpret_cast<float*>(xpart + (int64_t)a.T * V::PARTS * a.xrow);
+  int* plain = reinterpret_cast<int*>(fac + spans * 8 * NT);
 
-  // the first batch of weights starts before the tokens are staged; each of
-  // its places is refilled for the next batch as soon as it is used
-  typename V::Load held[BATCH];
-  int64_t tile = blockIdx.x;
-  auto fetch = [&](int64_t tl, int b, int i) {
-    const int sp = (b * BATCH + i) * VW + warp;
-    if (tl < tiles && sp < spans) V::load(a, tl * 16, k0 + sp * SPAN + 32 * t, g, held[i]);
+  // the copies' position: RING - 1 steps ahead of the arithmetic's
+  int64_t ctile = blockIdx.x;
+  int cstep = 0, cslot = 0;
+  typename V::Rows at = V::rows(a, ctile, k0, lane);
+  const int64_t inner = a.ldc * 2 - k0 - 32 * t;            // columns of codes from the lane's first on
+  auto copy_next = [&]() {
+    if (ctile < tiles) {
+      const int sp = PAIR * (cstep * VW + warp);
+#pragma unroll
+      for (int s = 0; s < PAIR; ++s)
+        V::copy(at, sp + s, sp + s < spans, (sp + s) * SPAN < inner, smem_u32(ring) + (cslot * PAIR + s) * RSLOT, lane);
+      if (++cstep == steps) {
+        cstep = 0;
+        ctile += gridDim.x;
+        if (ctile < tiles) at = V::rows(a, ctile, k0, lane);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++cslot == RING) cslot = 0;
   };
-#pragma unroll
-  for (int i = 0; i < BATCH; ++i) fetch(tile, 0, i);
+#pragma unroll 1
+  for (int i = 0; i < RING - 1; ++i) copy_next();
 
-  const int padded = spans * SPAN;
-  for (int tk = 0; tk < a.T; ++tk) {
-    uint8_t* row = xs + (int64_t)tk * V::PARTS * a.xrow;
-    for (int k = 8 * threadIdx.x; k < padded; k += 8 * VT) {
-      float f[8];
-      if (XF32) {
-        const float* src = static_cast<const float*>(a.x) + tk * a.ldx + k0 + k;
-        if (a.vec && k + 8 <= cols) {
-          const float4 u = reinterpret_cast<const float4*>(src)[0], v = reinterpret_cast<const float4*>(src)[1];
-          f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
-          f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
-        } else {
+  for (int i = threadIdx.x; i < spans * (8 * NT + 1); i += VT) fac[i] = 0.f;   // and plain
+  __syncthreads();
+  // a warp per token and span, a lane per four columns; four loads in flight
+  for (int u0 = warp; u0 < spans * a.T; u0 += 4 * VW) {
+    float f[4][4];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) f[c] = k + c < cols ? src[c] : 0.f;
+    for (int w = 0; w < 4; ++w) {
+      const int u = min(u0 + w * VW, spans * a.T - 1), sp = u / a.T, tk = u - sp * a.T;
+      const int k = sp * SPAN + 4 * lane;
+      const int64_t src = tk * a.ldx + k0 + k;
+      if (a.vec && k + 4 <= cols) {
+        if (XF32) {
+          const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + src);
+          f[w][0] = q.x; f[w][1] = q.y; f[w][2] = q.z; f[w][3] = q.w;
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + src);
+          f[w][0] = __uint_as_float(q.x << 16); f[w][1] = __uint_as_float(q.x & 0xFFFF0000u);
+          f[w][2] = __uint_as_float(q.y << 16); f[w][3] = __uint_as_float(q.y & 0xFFFF0000u);
         }
       } else {
-        const uint16_t* src = static_cast<const uint16_t*>(a.x) + tk * a.ldx + k0 + k;
-        if (a.vec && k + 8 <= cols) {
-          const uint4 u = *reinterpret_cast<const uint4*>(src);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int c = 0; c < 8; ++c) f[c] = __uint_as_float((c & 1) ? w[c >> 1] & 0xFFFF0000u : w[c >> 1] << 16);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) f[c] = k + c < cols ? __uint_as_float((uint32_t)src[c] << 16) : 0.f;
-        }
+        for (int c = 0; c < 4; ++c) f[w][c] = k + c < cols ? x_at(a, XF32, src + c) : 0.f;
       }
-      const int at = x_offset(k);
+    }
 #pragma unroll
-      for (int q = 0; q < V::PARTS; ++q) {
-        uint32_t h[8];
+    for (int w = 0; w < 4; ++w) {
+      const int u = u0 + w * VW;
+      if (u >= spans * a.T) break;
+      const int sp = u / a.T, tk = u - sp * a.T;
+      uint32_t big = 0, small = 0xFFFFFFFFu;     // magnitudes as bits; zeros are no smallest
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          // the top 8 bits, then the exact remainder scaled to its place; an
-          // infinity or a NaN stays in the first part
-          h[c] = __float_as_uint(f[c]) >> 16;
-          if (XF32) {
-            if (q == 0 && (h[c] & 0x7F80u) == 0x7F80u) {
-              if (f[c] != f[c]) h[c] |= 0x40u;
-              f[c] = 0.f;
-            } else {
-              f[c] = (f[c] - __uint_as_float(h[c] << 16)) * 256.f;
-            }
-          }
-        }
-        // register i of the piece: codes i (low half) and i + 4 (high half)
-        *reinterpret_cast<uint4*>(row + q * a.xrow + at) =
-            make_uint4(h[0] | (h[4] << 16), h[1] | (h[5] << 16), h[2] | (h[6] << 16), h[3] | (h[7] << 16));
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t b = __float_as_uint(f[w][c]) & 0x7FFFFFFFu;
+        big = max(big, b);
+        small = min(small, b - 1u);
+      }
+      big = __reduce_max_sync(0xffffffffu, big);
+      small = __reduce_min_sync(0xffffffffu, small);
+      const int e = (int)(big >> 23) - 127;      // [2^e, 2^(e+1)) holds the largest
+      // the range that fp16 parts cover, away from the ends of float32's
+      constexpr int kRange = XF32 ? 28 : 31;
+      const bool covered = big == 0 || (e >= -90 && e < 128 && (int)((small + 1u) >> 23) - 127 >= e - kRange);
+      const float up = covered && big ? __uint_as_float((uint32_t)(14 - e + 127) << 23) : 0.f;
+      if (lane == 0) {
+        fac[sp * 8 * NT + tk] =
+            covered && big ? __uint_as_float((uint32_t)(e - 14 - (FMT == KRONQ_MXFP4 ? kMxShift : 0) + 127) << 23) : 0.f;
+        if (!covered) plain[sp] = 1;
+      }
+      uint8_t* dst = xpart + (int64_t)tk * V::PARTS * a.xrow + x_offset(sp * SPAN + 4 * lane);
+      float r[4];
+      __half h[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float s = covered ? f[w][c] * up : 0.f;
+        h[c] = __float2half_rn(s);
+        r[c] = (s - __half2float(h[c])) * 2048.f;
+      }
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2((uint32_t)__half_as_ushort(h[0]) | ((uint32_t)__half_as_ushort(h[1]) << 16),
+                     (uint32_t)__half_as_ushort(h[2]) | ((uint32_t)__half_as_ushort(h[3]) << 16));
+      if (XF32) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) h[c] = __float2half_rn(r[c]);
+        *reinterpret_cast<uint2*>(dst + a.xrow) =
+            make_uint2((uint32_t)__half_as_ushort(h[0]) | ((uint32_t)__half_as_ushort(h[1]) << 16),
+                       (uint32_t)__half_as_ushort(h[2]) | ((uint32_t)__half_as_ushort(h[3]) << 16));
       }
     }
   }
   __syncthreads();
 
-  const float scale = 256.f, wg = !a.part && a.wg ? *a.wg : 1.f;
-  int buf = 0;
-  for (; tile < tiles; tile += gridDim.x, buf ^= 1) {
-    float acc[NT][V::PARTS][4] = {};
-    for (int b = 0; b < nb; ++b) {
-      const int64_t tl = b + 1 < nb ? tile : tile + gridDim.x;
-      const int bn = b + 1 < nb ? b + 1 : 0;
+  // columns of the mma beyond T read the last token: their sums are not stored
+  const uint8_t* xs[NT];
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        const int sp = (b * BATCH + i) * VW + warp;
-        if (sp < spans) V::step(a, held[i], k0 + sp * SPAN + 32 * t, xs + sp * 256 + 16 * t, g, acc);
-        fetch(tl, bn, i);
+  for (int nt = 0; nt < NT; ++nt) xs[nt] = xpart + (int64_t)min(8 * nt + g, a.T - 1) * V::PARTS * a.xrow + 16 * t;
+
+  const float wg = !a.part && a.wg ? *a.wg : 1.f;
+  int buf = 0, slot = 0;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    float acc[NT][4] = {};
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
+      __syncwarp();   // the other lanes' copies are in, and they are done with the slot that is copied to next
+      copy_next();
+      const int sp = PAIR * (i * VW + warp);
+      if (sp < spans) {
+        // a second span beyond the last has zero weights: any tokens do
+        const int has = sp + 1 < spans ? 1 : 0;
+        const uint8_t* xp[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) xp[nt] = xs[nt] + sp * 256;
+        typename V::Load v[PAIR];
+#pragma unroll
+        for (int s = 0; s < PAIR; ++s) v[s] = V::take(ring + (slot * PAIR + s) * RSLOT, lane);
+        V::step(a, v, k0 + sp * SPAN + 32 * t, k0 + cols, xp, has * 256, fac + sp * 8 * NT + 2 * t, has * 8 * NT,
+                (plain[sp] | plain[sp + has]) != 0, lane, acc);
       }
+      if (++slot == RING) slot = 0;
     }
     float* out = red[buf][warp];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v = acc[nt][0][e];
-        if (XF32) v = fmaf(acc[nt][V::PARTS - 1][e], 0x1p-16f, fmaf(acc[nt][V::PARTS / 2][e], 0x1p-8f, v));
-        // token-major: [token][row]
-        out[(8 * nt + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = v;
-      }
+      for (int e = 0; e < 4; ++e)   // token-major: [token][row]
+        out[(8 * nt + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = acc[nt][e];
     __syncthreads();
     for (int i = threadIdx.x; i < 16 * a.T; i += VT) {
       float v = red[buf][0][i];
@@ -310,7 +413,7 @@ __global__ void __launch_bounds__(VT, 2) fp4_matvec_kernel(const VecArgs a) {
         if (a.part) {
           a.part[((int64_t)blockIdx.y * a.T + tk) * a.m + r] = v;
         } else {
-          v = __fmul_rn(__fmul_rn(v, scale), wg);
+          v = __fmul_rn(v, wg);
           if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[tk * a.ldy + r] = __float2bfloat16_rn(v);
           else static_cast<float*>(a.y)[tk * a.ldy + r] = v;
         }
@@ -325,19 +428,21 @@ __global__ void __launch_bounds__(256) fp4_matvec_join_kernel(const VecArgs a, i
   if (i >= total) return;
   float v = 0.f;
   for (int s = 0; s < slices; ++s) v += a.part[s * total + i];
-  v = __fmul_rn(__fmul_rn(v, 256.f), a.wg ? *a.wg : 1.f);
+  v = __fmul_rn(v, a.wg ? *a.wg : 1.f);
   const int64_t tk = i / a.m, r = i - tk * a.m;
   if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[tk * a.ldy + r] = __float2bfloat16_rn(v);
   else static_cast<float*>(a.y)[tk * a.ldy + r] = v;
 }
 
+// Shared memory of a span's factors and its float32 flag.
+int span_bytes(int64_t T) { return (T > 8 ? 17 : 9) * 4; }
+
 // Columns of a slice: as many as leave room for the tokens' parts, fewer
 // where there are not enough row tiles for the SMs.
 int64_t slice_columns(int64_t T, int64_t m, int64_t n, bool x_f32) {
-  const int64_t bytes = T * (x_f32 ? 6 : 2);
-  int64_t most = XSMEM / bytes / SPAN * SPAN;
+  const int64_t bytes = T * (x_f32 ? 4 : 2) * SPAN + span_bytes(T);
   const int64_t spans = ceil_div(n, SPAN);
-  int64_t slices = ceil_div(spans * SPAN, most);
+  int64_t slices = ceil_div(spans, XSMEM / bytes);
   const int64_t tiles = ceil_div(m, 16);
   while (tiles * slices < 148 && ceil_div(spans, 2 * slices) * SPAN >= 4096) slices *= 2;
   return ceil_div(spans, slices) * SPAN;
@@ -370,7 +475,7 @@ kronq_status fp4_matvec(const Fp4Matvec& v, int fmt, cudaStream_t st) {
   a.kslice = (int)kslice;
   a.xrow = (int)kslice * 2 + 64;   // a token's row is shifted by half of the banks against its neighbour's
   const int esize = v.x_f32 ? 4 : 2;
-  a.vec = aligned(v.x, 16) && (v.ldx * esize) % 16 == 0;
+  a.vec = aligned(v.x, 4 * esize) && v.ldx % 4 == 0;
   a.y = v.y; a.y_bf16 = v.y_bf16; a.ldy = v.ldy;
   a.part = slices > 1 ? static_cast<float*>(v.workspace) : nullptr;
   const int64_t tiles = ceil_div(v.m, 16);
@@ -378,7 +483,7 @@ kronq_status fp4_matvec(const Fp4Matvec& v, int fmt, cudaStream_t st) {
   if (gx < 1) gx = 1;
   if (gx > tiles) gx = tiles;
   const dim3 grid((unsigned)gx, (unsigned)slices);
-  const int smem = (int)(v.T * (v.x_f32 ? 3 : 1)) * a.xrow;
+  const int smem = RBYTES + (int)(v.T * (v.x_f32 ? 2 : 1)) * a.xrow + (int)(kslice / SPAN) * span_bytes(v.T);
   kronq_status r;
   if (fmt == KRONQ_MXFP4) r = v.x_f32 ? launch_vec<KRONQ_MXFP4, true>(a, grid, smem, st) : launch_vec<KRONQ_MXFP4, false>(a, grid, smem, st);
   else r = v.x_f32 ? launch_vec<KRONQ_NVFP4, true>(a, grid, smem, st) : launch_vec<KRONQ_NVFP4, false>(a, grid, smem, st);
