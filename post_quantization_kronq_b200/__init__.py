@@ -312,8 +312,16 @@ def kronq_kfac_loss(E, HG, ws=None, stream=None) -> float:
 
 # ------------------------------------------------------------ microscaled 4-bit floating point
 # These calls run once per layer and decoded token, so their marshalling is
-# kept short: plain integers for pointers, sizes worked out here.
-_FP4_ROW_DIVISOR = (512, 256)    # columns of 16 scale bytes: MXFP4, NVFP4
+# kept short: plain integers for pointers, sizes worked out here, torch looked
+# up once.
+_torch = None
+
+
+def _fp4_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
 
 
 def kronq_fp4_code_row_bytes(n: int) -> int:
@@ -326,17 +334,18 @@ def kronq_fp4_scale_row_bytes(fmt: int, n: int) -> int:
 
 def _fp4_call(fn, device, stream, *args):
     """One library call with the tensors' device current, on the given stream or that device's current one."""
-    import torch
+    cuda = (_torch or _fp4_torch())._C
+    index = device.index
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        raw = cuda._cuda_getCurrentRawStream(index)
     elif stream.device == device:
         raw = stream.cuda_stream
     else:
         raise ValueError(f"stream of {stream.device} for tensors on {device}")
-    if torch.cuda.current_device() == device.index:
+    if cuda._cuda_getDevice() == index:
         status = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with _torch.cuda.device(device):
             status = fn(*args, raw)
     if status:
         check(status)
@@ -344,26 +353,32 @@ def _fp4_call(fn, device, stream, *args):
 
 def _fp4_matrix(t, name):
     """(pointer, rows, columns, row stride) of a device matrix with dense rows."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be a matrix with unit stride along its rows")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live in device memory")
-    rows, n = shape
-    return t.data_ptr(), rows, n, stride[0] if rows > 1 else max(stride[0], n)
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a matrix in device memory")
+    rows, n = t.shape
+    ld, one = t.stride()
+    if one != 1 and n > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    return t.data_ptr(), rows, n, ld if rows > 1 and ld > 0 else max(ld, n)
 
 
 def _fp4_pair(codes, scales, name, fmt, lead, n, device):
     """Pointers of a quantised matrix's codes and scales, whose shapes are lead + (row bytes,)."""
-    if fmt != MXFP4 and fmt != NVFP4:
+    if fmt == NVFP4:
+        shape = lead + (((n + 255) >> 8) << 4,)
+    elif fmt == MXFP4:
+        shape = lead + (((n + 511) >> 9) << 4,)
+    else:
         raise ValueError("fmt must be MXFP4 or NVFP4")
-    for t, what, width in ((codes, "codes", (n + 31) // 32 * 16),
-                           (scales, "scales", -(-n // _FP4_ROW_DIVISOR[fmt]) * 16)):
-        if t.element_size() != 1 or t.is_floating_point() or t.shape != lead + (width,) or not t.is_contiguous():
-            raise ValueError(f"{name} {what} must be contiguous uint8 of shape {lead + (width,)}, got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} {what} must live on {device}")
+    uint8 = (_torch or _fp4_torch()).uint8
+    if codes.shape != lead + (((n + 31) >> 5) << 4,) or codes.dtype is not uint8 or not codes.is_contiguous():
+        raise ValueError(f"{name} codes must be contiguous uint8 of shape {lead + (((n + 31) >> 5) << 4,)}, got "
+                         f"{codes.dtype} {tuple(codes.shape)}")
+    if scales.shape != shape or scales.dtype is not uint8 or not scales.is_contiguous():
+        raise ValueError(f"{name} scales must be contiguous uint8 of shape {shape}, got {scales.dtype} "
+                         f"{tuple(scales.shape)}")
+    if codes.device != device or scales.device != device:
+        raise ValueError(f"{name} must live on {device}")
     return codes.data_ptr(), scales.data_ptr()
 
 
@@ -374,8 +389,7 @@ def _fp4_scale(t, name, fmt, count, device):
         return None
     if fmt != NVFP4:
         raise ValueError(f"{name}: MXFP4 has no tensor scale")
-    import torch
-    if t.dtype != torch.float32 or t.numel() != count or t.device != device or not t.is_contiguous():
+    if t.dtype is not _torch.float32 or t.numel() != count or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must hold {count} float32 on {device}")
     return t.data_ptr()
 
@@ -390,6 +404,15 @@ def _fp4_ws(ws, need, args, device):
     elif ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous on {device}")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _fp4_dtype(t):
+    dt = t.dtype
+    if dt is _torch.bfloat16:
+        return BF16
+    if dt is _torch.float32:
+        return F32
+    raise TypeError(f"unsupported dtype {dt}")
 
 
 def kronq_fp4_quantize_workspace_bytes(rows: int, n: int, fmt: int) -> int:
@@ -412,7 +435,7 @@ def kronq_fp4_quantize(x, fmt: int, codes, scales, gscale=None, gscale_given: bo
     pw, nw = None, 0
     if pg is not None and not gscale_given:
         pw, nw, ws = _fp4_ws(ws, kronq_fp4_quantize_workspace_bytes, (rows, n, fmt), dev)
-    _fp4_call(lib.kronq_fp4_quantize, dev, stream, px, _dtype_code(x), rows, n, ldx, fmt, pc, ps, pg,
+    _fp4_call(lib.kronq_fp4_quantize, dev, stream, px, _fp4_dtype(x), rows, n, ldx, fmt, pc, ps, pg,
               1 if gscale_given else 0, pd, ldd, pw, nw)
 
 
@@ -422,7 +445,7 @@ def kronq_fp4_dequantize(codes, scales, fmt: int, out, gscale=None, stream=None)
     dev = out.device
     pc, ps = _fp4_pair(codes, scales, "input", fmt, (rows,), n, dev)
     pg = _fp4_scale(gscale, "gscale", fmt, 1, dev)
-    _fp4_call(lib.kronq_fp4_dequantize, dev, stream, pc, ps, pg, fmt, rows, n, po, _dtype_code(out), ldo)
+    _fp4_call(lib.kronq_fp4_dequantize, dev, stream, pc, ps, pg, fmt, rows, n, po, _fp4_dtype(out), ldo)
 
 
 def kronq_fp4_matmul_workspace_bytes(T: int, m: int, n: int, fmt: int) -> int:
@@ -438,7 +461,7 @@ def kronq_fp4_matmul(xc, xs, wc, wsc, fmt: int, n: int, y, xg=None, wg=None, ws=
     pwc, pws = _fp4_pair(wc, wsc, "W", fmt, (m,), n, dev)
     pxg, pwg = _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, 1, dev)
     pw, nw, ws = _fp4_ws(ws, kronq_fp4_matmul_workspace_bytes, (T, m, n, fmt), dev)
-    _fp4_call(lib.kronq_fp4_matmul, dev, stream, pxc, pxs, pxg, pwc, pws, pwg, fmt, T, m, n, py, _dtype_code(y),
+    _fp4_call(lib.kronq_fp4_matmul, dev, stream, pxc, pxs, pxg, pwc, pws, pwg, fmt, T, m, n, py, _fp4_dtype(y),
               ldy, pw, nw)
 
 
@@ -457,8 +480,8 @@ def kronq_fp4_matvec(x, wc, wsc, fmt: int, y, wg=None, ws=None, stream=None):
     pwc, pws = _fp4_pair(wc, wsc, "W", fmt, (m,), n, dev)
     pwg = _fp4_scale(wg, "wg", fmt, 1, dev)
     pw, nw, ws = _fp4_ws(ws, kronq_fp4_matvec_workspace_bytes, (T, m, n, fmt), dev)
-    _fp4_call(lib.kronq_fp4_matvec, dev, stream, px, _dtype_code(x), ldx, pwc, pws, pwg, fmt, T, m, n, py,
-              _dtype_code(y), ldy, pw, nw)
+    _fp4_call(lib.kronq_fp4_matvec, dev, stream, px, _fp4_dtype(x), ldx, pwc, pws, pwg, fmt, T, m, n, py,
+              _fp4_dtype(y), ldy, pw, nw)
 
 
 def kronq_fp4_grouped_matmul(xc, xs, offsets, wc, wsc, fmt: int, n: int, y, xg=None, wg=None, stream=None):
@@ -475,4 +498,4 @@ def kronq_fp4_grouped_matmul(xc, xs, offsets, wc, wsc, fmt: int, n: int, y, xg=N
     pwc, pws = _fp4_pair(wc, wsc, "W", fmt, (E, m), n, dev)
     pxg, pwg = _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, E, dev)
     _fp4_call(lib.kronq_fp4_grouped_matmul, dev, stream, pxc, pxs, pxg, offsets.data_ptr(), E, pwc, pws, pwg, fmt, T,
-              m, n, py, _dtype_code(y), ldy)
+              m, n, py, _fp4_dtype(y), ldy)

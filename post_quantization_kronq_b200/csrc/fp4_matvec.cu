@@ -2,12 +2,14 @@
 // (single-token decode): y[t, r] = g sum_k x[t, k] W[r, k], at most 16 tokens.
 //
 // Bound by HBM: each weight is 4 bits plus its share of a scale and is used
-// once per token.  A CTA of eight warps owns 16 rows at a time, the warps
-// split the columns in interleaved spans of 128 (lane t of a row's four takes
-// 16 bytes of codes, 32 weights).  Each warp copies its spans into a ring of
-// its own in shared memory with cp.async, RING spans ahead and on into the
-// next rows: loads into registers this far ahead share the warp's few
-// scoreboards, and a wait for the first became one for the last.  The products run on mma.sync (m16n8k16, fp16 in, float32 out),
+// once per token.  Eight warps of a CTA split the columns in interleaved spans
+// of 128 (lane t of a row's four takes 16 bytes of codes, 32 weights); a warp
+// works on 16 rows at a time.  A slice of few spans (many tokens fill the
+// shared memory) gives the spare warps other rows.  Each warp copies its spans
+// into a ring of its own in shared memory with cp.async, RING - 1 pairs ahead
+// and on into its next rows: loads into registers this far ahead share the
+// warp's few scoreboards, and a wait for the first became one for the last
+// (61 us against 41 us for 28672 x 8192 NVFP4 and one token).  The products run on mma.sync (m16n8k16, fp16 in, float32 out),
 // rows on the M side, tokens on the N side: one weight load serves 8 tokens
 // at the price of one.
 //
@@ -37,11 +39,12 @@ namespace {
 
 constexpr int VT = 256, VW = VT / 32;
 constexpr int SPAN = 128;                 // columns of one step of a warp
-constexpr int PAIR = 2;                   // spans of a step: two independent chains of mma
+constexpr int PAIR = 2;                   // neighbouring spans of a step: independent chains of mma
 constexpr int RING = 3;                   // steps of a warp in shared memory
 constexpr int RSLOT = 16 * SPAN / 2 + 16 * 8;   // codes of 16 rows, up to 8 scale bytes of each
 constexpr int RBYTES = VW * RING * PAIR * RSLOT;
-constexpr int XSMEM = 40 * 1024;          // most shared memory for tokens: two CTAs on an SM
+constexpr int CTAS = 2;                   // on an SM
+constexpr int XSMEM = 40 * 1024;          // shared memory of each for tokens
 
 struct VecArgs {
   const void* x;
@@ -51,6 +54,7 @@ struct VecArgs {
   int T;
   int64_t m, n, ldc, lds;
   int kslice;             // columns of a slice, a multiple of SPAN (grid.y slices)
+  int wk;                 // warps that split a slice's columns (1, 2, 4 or 8); the others take other rows
   int xrow;               // bytes of a token's part in shared memory
   int vec;                // 4-element loads of x
   void* y;
@@ -94,33 +98,40 @@ struct Vec {
     uint4 w[2];
     uint32_t s[2];
   };
-  // What a lane copies of a tile: 16 bytes of codes of rows g and g + 8, and
-  // four scale bytes of one row (NVFP4: lane / 2, MXFP4: lane, of the first 16).
+  // What a lane copies of a row tile: 16 bytes of codes of rows g and g + 8,
+  // and four scale bytes of one row (NVFP4: lane / 2, MXFP4: lane, of the
+  // first 16); pointers to the span that is copied next.
   struct Rows {
     const uint8_t *c[2], *s;
   };
-  static __device__ __forceinline__ Rows rows(const VecArgs& a, int64_t tile, int64_t k0, int lane) {
+  static __device__ __forceinline__ Rows rows(const VecArgs& a, int64_t tile, int64_t k, int lane) {
     Rows p;
 #pragma unroll
     for (int h = 0; h < 2; ++h)   // rows beyond m read the last one: their results are not stored
-      p.c[h] = a.wc + min(tile * 16 + (lane >> 2) + 8 * h, a.m - 1) * a.ldc + (k0 >> 1) + 16 * (lane & 3);
+      p.c[h] = a.wc + min(tile * 16 + (lane >> 2) + 8 * h, a.m - 1) * a.ldc + (k >> 1) + 16 * (lane & 3);
     const int row = BPL == 2 ? lane >> 1 : lane & 15;
-    p.s = a.ws + min(tile * 16 + row, a.m - 1) * a.lds + k0 / (32 / BPL) + (BPL == 2 ? 4 * (lane & 1) : 0);
+    p.s = a.ws + min(tile * 16 + row, a.m - 1) * a.lds + k / (32 / BPL) + (BPL == 2 ? 4 * (lane & 1) : 0);
     return p;
   }
-  // Span sp into a ring slot, zeros where it is not there (`there`) or the
-  // lane's codes do not lie within the row (`inside`).
-  static __device__ __forceinline__ void copy(const Rows& p, int sp, bool there, bool inside, uint32_t slot, int lane) {
-    const int n = there && inside ? 16 : 0;
+  // The pair of spans into a ring slot: zeros where the lane's codes do not lie
+  // within the row, and for a second span beyond the slice (`left`: columns
+  // from the lane's first on of the row, of the slice; a copy of nothing names
+  // the first row).
+  static __device__ __forceinline__ void copy(const VecArgs& a, const Rows& p, int row_left, int slice_left, uint32_t slot,
+                                              int lane) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + 512 * h + 16 * lane),
-                   "l"(p.c[h] + (n ? sp * (SPAN / 2) : 0)), "r"(n)
-                   : "memory");
-    if (BPL == 2 || lane < 16)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot + 1024 + 4 * lane),
-                   "l"(p.s + (there ? sp * (4 * BPL) : 0)), "r"(there ? 4 : 0)
-                   : "memory");
+    for (int s = 0; s < PAIR; ++s) {
+      const bool there = s * SPAN < slice_left, in = there && s * SPAN < row_left;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + s * RSLOT + 512 * h + 16 * lane),
+                     "l"(in ? p.c[h] + s * (SPAN / 2) : a.wc), "r"(in ? 16 : 0)
+                     : "memory");
+      if (BPL == 2 || lane < 16)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot + s * RSLOT + 1024 + 4 * lane),
+                     "l"(there ? p.s + s * (4 * BPL) : a.ws), "r"(there ? 4 : 0)
+                     : "memory");
+    }
   }
   static __device__ __forceinline__ Load take(const uint8_t* slot, int lane) {
     Load v;
@@ -256,8 +267,48 @@ __device__ __forceinline__ int x_offset(int k) {
   return (k / SPAN) * 256 + j * 64 + t * 16 + (k & 7) * 2;
 }
 
+// One span of a token into shared memory (a warp, a lane per four columns):
+// scaled to fp16 parts; its factor, or false where fp16 does not cover it.
+template <int FMT, bool XF32>
+__device__ __forceinline__ bool stage_span(const float (&f)[4], uint8_t* dst, int xrow, float& factor) {
+  uint32_t big = 0, small = 0xFFFFFFFFu;     // magnitudes as bits; zeros are no smallest
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t b = __float_as_uint(f[c]) & 0x7FFFFFFFu;
+    big = max(big, b);
+    small = min(small, b - 1u);
+  }
+  big = __reduce_max_sync(0xffffffffu, big);
+  small = __reduce_min_sync(0xffffffffu, small);
+  const int e = (int)(big >> 23) - 127;      // [2^e, 2^(e+1)) holds the largest
+  // the range that fp16 parts cover, away from the ends of float32's
+  constexpr int kRange = XF32 ? 28 : 31;
+  const bool covered = big == 0 || (e >= -90 && e < 128 && (int)((small + 1u) >> 23) - 127 >= e - kRange);
+  const float up = covered && big ? __uint_as_float((uint32_t)(14 - e + 127) << 23) : 0.f;
+  factor = covered && big ? __uint_as_float((uint32_t)(e - 14 - (FMT == KRONQ_MXFP4 ? kMxShift : 0) + 127) << 23) : 0.f;
+  float r[4];
+  __half h[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float s = covered ? f[c] * up : 0.f;
+    h[c] = __float2half_rn(s);
+    r[c] = (s - __half2float(h[c])) * 2048.f;
+  }
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2((uint32_t)__half_as_ushort(h[0]) | ((uint32_t)__half_as_ushort(h[1]) << 16),
+                 (uint32_t)__half_as_ushort(h[2]) | ((uint32_t)__half_as_ushort(h[3]) << 16));
+  if (XF32) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) h[c] = __float2half_rn(r[c]);
+    *reinterpret_cast<uint2*>(dst + xrow) =
+        make_uint2((uint32_t)__half_as_ushort(h[0]) | ((uint32_t)__half_as_ushort(h[1]) << 16),
+                   (uint32_t)__half_as_ushort(h[2]) | ((uint32_t)__half_as_ushort(h[3]) << 16));
+  }
+  return covered;
+}
+
 template <int FMT, bool XF32, int NT>
-__global__ void __launch_bounds__(VT, 2) fp4_matvec_kernel(const VecArgs a) {
+__global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
   using V = Vec<FMT, XF32, NT>;
   // the warps' rings, the tokens' parts, then per span the factors of 8 NT
   // tokens and whether the span is computed in float32
@@ -267,104 +318,76 @@ __global__ void __launch_bounds__(VT, 2) fp4_matvec_kernel(const VecArgs a) {
   const int64_t k0 = (int64_t)blockIdx.y * a.kslice;
   const int cols = (int)min((int64_t)a.kslice, a.n - k0);
   const int spans = (cols + SPAN - 1) / SPAN;
-  const int steps = (spans + PAIR * VW - 1) / (PAIR * VW);  // of a warp for a row tile
-  const int64_t tiles = (a.m + 15) / 16;
+  const int wk = a.wk, wr = VW / wk;                        // warps along the columns, along the rows
+  const int kw = warp & (wk - 1), rw = warp / wk;
+  const int64_t tiles = (a.m + 15) / 16, hop = (int64_t)gridDim.x * wr;
   uint8_t* ring = xsm + warp * (RING * PAIR * RSLOT);
   uint8_t* xpart = xsm + RBYTES;
   float* fac = reinterpret_cast<float*>(xpart + (int64_t)a.T * V::PARTS * a.xrow);
   int* plain = reinterpret_cast<int*>(fac + spans * 8 * NT);
 
   // the copies' position: RING - 1 steps ahead of the arithmetic's
-  int64_t ctile = blockIdx.x;
-  int cstep = 0, cslot = 0;
-  typename V::Rows at = V::rows(a, ctile, k0, lane);
-  const int64_t inner = a.ldc * 2 - k0 - 32 * t;            // columns of codes from the lane's first on
+  const int hop_k = wk * PAIR;                              // spans from a warp's step to its next
+  int64_t ctile = (int64_t)blockIdx.x * wr + rw;
+  int cspan = kw * PAIR;
+  uint32_t cslot = smem_u32(ring);
+  typename V::Rows at = V::rows(a, ctile, k0 + cspan * SPAN, lane);
+  const int row_left = (int)min(a.ldc * 2 - k0 - 32 * t, (int64_t)1 << 30);
   auto copy_next = [&]() {
-    if (ctile < tiles) {
-      const int sp = PAIR * (cstep * VW + warp);
+    if (ctile < tiles && cspan < spans) {
+      V::copy(a, at, row_left - cspan * SPAN, (spans - cspan) * SPAN, cslot, lane);
+      cspan += hop_k;
 #pragma unroll
-      for (int s = 0; s < PAIR; ++s)
-        V::copy(at, sp + s, sp + s < spans, (sp + s) * SPAN < inner, smem_u32(ring) + (cslot * PAIR + s) * RSLOT, lane);
-      if (++cstep == steps) {
-        cstep = 0;
-        ctile += gridDim.x;
-        if (ctile < tiles) at = V::rows(a, ctile, k0, lane);
+      for (int h = 0; h < 2; ++h) at.c[h] += hop_k * (SPAN / 2);
+      at.s += hop_k * (4 * V::BPL);
+      if (cspan >= spans) {
+        cspan = kw * PAIR;
+        ctile += hop;
+        if (ctile < tiles) at = V::rows(a, ctile, k0 + cspan * SPAN, lane);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (++cslot == RING) cslot = 0;
+    cslot += PAIR * RSLOT;
+    if (cslot == smem_u32(ring) + RING * PAIR * RSLOT) cslot = smem_u32(ring);
   };
 #pragma unroll 1
   for (int i = 0; i < RING - 1; ++i) copy_next();
 
-  for (int i = threadIdx.x; i < spans * (8 * NT + 1); i += VT) fac[i] = 0.f;   // and plain
-  __syncthreads();
-  // a warp per token and span, a lane per four columns; four loads in flight
-  for (int u0 = warp; u0 < spans * a.T; u0 += 4 * VW) {
-    float f[4][4];
+  // a warp per span, four tokens' loads in flight
+  for (int sp = warp; sp < spans; sp += VW) {
+    const int k = sp * SPAN + 4 * lane;
+    uint8_t* dst = xpart + x_offset(k);
+    bool covered = true;
+    for (int tk0 = 0; tk0 < a.T; tk0 += 4) {
+      float f[4][4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int u = min(u0 + w * VW, spans * a.T - 1), sp = u / a.T, tk = u - sp * a.T;
-      const int k = sp * SPAN + 4 * lane;
-      const int64_t src = tk * a.ldx + k0 + k;
-      if (a.vec && k + 4 <= cols) {
-        if (XF32) {
-          const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + src);
-          f[w][0] = q.x; f[w][1] = q.y; f[w][2] = q.z; f[w][3] = q.w;
+      for (int w = 0; w < 4; ++w) {
+        const int64_t src = (int64_t)min(tk0 + w, a.T - 1) * a.ldx + k0 + k;
+        if (a.vec && k + 4 <= cols) {
+          if (XF32) {
+            const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + src);
+            f[w][0] = q.x; f[w][1] = q.y; f[w][2] = q.z; f[w][3] = q.w;
+          } else {
+            const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + src);
+            f[w][0] = __uint_as_float(q.x << 16); f[w][1] = __uint_as_float(q.x & 0xFFFF0000u);
+            f[w][2] = __uint_as_float(q.y << 16); f[w][3] = __uint_as_float(q.y & 0xFFFF0000u);
+          }
         } else {
-          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + src);
-          f[w][0] = __uint_as_float(q.x << 16); f[w][1] = __uint_as_float(q.x & 0xFFFF0000u);
-          f[w][2] = __uint_as_float(q.y << 16); f[w][3] = __uint_as_float(q.y & 0xFFFF0000u);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) f[w][c] = k + c < cols ? x_at(a, XF32, src + c) : 0.f;
         }
-      } else {
+      }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) f[w][c] = k + c < cols ? x_at(a, XF32, src + c) : 0.f;
+      for (int w = 0; w < 4; ++w) {
+        if (tk0 + w < a.T) {
+          float factor;
+          covered &= stage_span<FMT, XF32>(f[w], dst + (int64_t)(tk0 + w) * V::PARTS * a.xrow, a.xrow, factor);
+          if (lane == 0) fac[sp * 8 * NT + tk0 + w] = factor;
+        }
       }
     }
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const int u = u0 + w * VW;
-      if (u >= spans * a.T) break;
-      const int sp = u / a.T, tk = u - sp * a.T;
-      uint32_t big = 0, small = 0xFFFFFFFFu;     // magnitudes as bits; zeros are no smallest
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t b = __float_as_uint(f[w][c]) & 0x7FFFFFFFu;
-        big = max(big, b);
-        small = min(small, b - 1u);
-      }
-      big = __reduce_max_sync(0xffffffffu, big);
-      small = __reduce_min_sync(0xffffffffu, small);
-      const int e = (int)(big >> 23) - 127;      // [2^e, 2^(e+1)) holds the largest
-      // the range that fp16 parts cover, away from the ends of float32's
-      constexpr int kRange = XF32 ? 28 : 31;
-      const bool covered = big == 0 || (e >= -90 && e < 128 && (int)((small + 1u) >> 23) - 127 >= e - kRange);
-      const float up = covered && big ? __uint_as_float((uint32_t)(14 - e + 127) << 23) : 0.f;
-      if (lane == 0) {
-        fac[sp * 8 * NT + tk] =
-            covered && big ? __uint_as_float((uint32_t)(e - 14 - (FMT == KRONQ_MXFP4 ? kMxShift : 0) + 127) << 23) : 0.f;
-        if (!covered) plain[sp] = 1;
-      }
-      uint8_t* dst = xpart + (int64_t)tk * V::PARTS * a.xrow + x_offset(sp * SPAN + 4 * lane);
-      float r[4];
-      __half h[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float s = covered ? f[w][c] * up : 0.f;
-        h[c] = __float2half_rn(s);
-        r[c] = (s - __half2float(h[c])) * 2048.f;
-      }
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2((uint32_t)__half_as_ushort(h[0]) | ((uint32_t)__half_as_ushort(h[1]) << 16),
-                     (uint32_t)__half_as_ushort(h[2]) | ((uint32_t)__half_as_ushort(h[3]) << 16));
-      if (XF32) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) h[c] = __float2half_rn(r[c]);
-        *reinterpret_cast<uint2*>(dst + a.xrow) =
-            make_uint2((uint32_t)__half_as_ushort(h[0]) | ((uint32_t)__half_as_ushort(h[1]) << 16),
-                       (uint32_t)__half_as_ushort(h[2]) | ((uint32_t)__half_as_ushort(h[3]) << 16));
-      }
-    }
+    if (lane >= a.T && lane < 8 * NT) fac[sp * 8 * NT + lane] = 0.f;
+    if (lane == 0) plain[sp] = !covered;
   }
   __syncthreads();
 
@@ -375,15 +398,14 @@ __global__ void __launch_bounds__(VT, 2) fp4_matvec_kernel(const VecArgs a) {
 
   const float wg = !a.part && a.wg ? *a.wg : 1.f;
   int buf = 0, slot = 0;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+  for (int64_t tile0 = (int64_t)blockIdx.x * wr; tile0 < tiles; tile0 += hop, buf ^= 1) {
     float acc[NT][4] = {};
+    if (tile0 + rw < tiles) {
 #pragma unroll 1
-    for (int i = 0; i < steps; ++i) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
-      __syncwarp();   // the other lanes' copies are in, and they are done with the slot that is copied to next
-      copy_next();
-      const int sp = PAIR * (i * VW + warp);
-      if (sp < spans) {
+      for (int sp = kw * PAIR; sp < spans; sp += hop_k) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
+        __syncwarp();   // the other lanes' copies are in, and they are done with the slot that is copied to next
+        copy_next();
         // a second span beyond the last has zero weights: any tokens do
         const int has = sp + 1 < spans ? 1 : 0;
         const uint8_t* xp[NT];
@@ -394,8 +416,8 @@ __global__ void __launch_bounds__(VT, 2) fp4_matvec_kernel(const VecArgs a) {
         for (int s = 0; s < PAIR; ++s) v[s] = V::take(ring + (slot * PAIR + s) * RSLOT, lane);
         V::step(a, v, k0 + sp * SPAN + 32 * t, k0 + cols, xp, has * 256, fac + sp * 8 * NT + 2 * t, has * 8 * NT,
                 (plain[sp] | plain[sp + has]) != 0, lane, acc);
+        if (++slot == RING) slot = 0;
       }
-      if (++slot == RING) slot = 0;
     }
     float* out = red[buf][warp];
 #pragma unroll
@@ -404,11 +426,11 @@ __global__ void __launch_bounds__(VT, 2) fp4_matvec_kernel(const VecArgs a) {
       for (int e = 0; e < 4; ++e)   // token-major: [token][row]
         out[(8 * nt + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = acc[nt][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * a.T; i += VT) {
-      float v = red[buf][0][i];
-#pragma unroll
-      for (int w = 1; w < VW; ++w) v += red[buf][w][i];
-      const int64_t r = tile * 16 + (i & 15), tk = i >> 4;
+    for (int i = threadIdx.x; i < 16 * a.T * wr; i += VT) {
+      const int part = i / (16 * a.T), in = i - part * 16 * a.T;
+      float v = red[buf][part * wk][in];
+      for (int w = 1; w < wk; ++w) v += red[buf][part * wk + w][in];
+      const int64_t r = (tile0 + part) * 16 + (in & 15), tk = in >> 4;
       if (r < a.m) {
         if (a.part) {
           a.part[((int64_t)blockIdx.y * a.T + tk) * a.m + r] = v;
@@ -420,6 +442,7 @@ __global__ void __launch_bounds__(VT, 2) fp4_matvec_kernel(const VecArgs a) {
       }
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // y = the slices' partial sums in order, scaled.
@@ -478,10 +501,12 @@ kronq_status fp4_matvec(const Fp4Matvec& v, int fmt, cudaStream_t st) {
   a.vec = aligned(v.x, 4 * esize) && v.ldx % 4 == 0;
   a.y = v.y; a.y_bf16 = v.y_bf16; a.ldy = v.ldy;
   a.part = slices > 1 ? static_cast<float*>(v.workspace) : nullptr;
-  const int64_t tiles = ceil_div(v.m, 16);
-  int64_t gx = 2 * (int64_t)sm_count() / slices;
+  a.wk = VW;
+  while (a.wk > 1 && a.wk * PAIR > ceil_div(kslice, SPAN * PAIR) * PAIR) a.wk /= 2;
+  const int64_t groups = ceil_div(ceil_div(v.m, 16), VW / a.wk);   // row tiles that a CTA takes at once
+  int64_t gx = CTAS * (int64_t)sm_count() / slices;
   if (gx < 1) gx = 1;
-  if (gx > tiles) gx = tiles;
+  if (gx > groups) gx = groups;
   const dim3 grid((unsigned)gx, (unsigned)slices);
   const int smem = RBYTES + (int)(v.T * (v.x_f32 ? 2 : 1)) * a.xrow + (int)(kslice / SPAN) * span_bytes(v.T);
   kronq_status r;
