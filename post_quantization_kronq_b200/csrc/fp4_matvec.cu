@@ -113,6 +113,20 @@ struct Vec {
     p.s = a.ws + min(tile * 16 + row, a.m - 1) * a.lds + k / (32 / BPL) + (BPL == 2 ? 4 * (lane & 1) : 0);
     return p;
   }
+  // A pair of whole spans into a ring slot.
+  static __device__ __forceinline__ void copy_whole(const Rows& p, uint32_t slot, int lane) {
+    const uint32_t code = slot + 16 * lane, scale = slot + 1024 + 4 * lane;
+    asm volatile(
+        "cp.async.cg.shared.global [%0], [%1], 16;\n\tcp.async.cg.shared.global [%0 + 512], [%2], 16;\n\t"
+        "cp.async.cg.shared.global [%0 + %3], [%1 + %4], 16;\n\tcp.async.cg.shared.global [%0 + %5], [%2 + %4], 16;" ::"r"(code),
+        "l"(p.c[0]), "l"(p.c[1]), "n"(RSLOT), "n"(SPAN / 2), "n"(RSLOT + 512)
+        : "memory");
+    if (BPL == 2 || lane < 16)
+      asm volatile(
+          "cp.async.ca.shared.global [%0], [%1], 4;\n\tcp.async.ca.shared.global [%0 + %2], [%1 + %3], 4;" ::"r"(scale),
+          "l"(p.s), "n"(RSLOT), "n"(4 * BPL)
+          : "memory");
+  }
   // The pair of spans into a ring slot: zeros where the lane's codes do not lie
   // within the row, and for a second span beyond the slice (`left`: columns
   // from the lane's first on of the row, of the slice; a copy of nothing names
@@ -145,20 +159,21 @@ struct Vec {
     return v;
   }
 
-  // Multipliers of the lane's blocks (its columns begin at k; those from kend
-  // on count as zero); true where one is beyond what fp16 takes.
-  static __device__ __forceinline__ bool multipliers(const Load& v, int64_t k, int64_t kend, uint32_t (&mul)[2][BPL]) {
+  // Multipliers of the lane's blocks, of which `left` columns are there (the
+  // others count as zero); true where one is beyond what fp16 takes.
+  template <bool WHOLE>
+  static __device__ __forceinline__ bool multipliers(const Load& v, int left, uint32_t (&mul)[2][BPL]) {
     bool odd = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (FMT == KRONQ_NVFP4) {
         uint32_t two = v.s[h], f;
-        if (k + 32 > kend) two = k >= kend ? 0u : k + 16 >= kend ? two & 0xFFu : two;
+        if (!WHOLE && left < 32) two = left <= 0 ? 0u : left <= 16 ? two & 0xFFu : two;
         asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(f) : "r"(two));
         mul[h][0] = __byte_perm(f, f, 0x1010);
         mul[h][BPL - 1] = __byte_perm(f, f, 0x3232);
       } else {
-        const bool in = k < kend;
+        const bool in = WHOLE || left > 0;
         odd |= in && (v.s[h] < kMxLow || v.s[h] > kMxHigh);
         // fp16 2^(byte - 127 + 12), subnormal below 2^-14
         const int e = (int)v.s[h] - 127 + kMxShift + 15;
@@ -169,20 +184,20 @@ struct Vec {
     return odd;
   }
 
-  // acc += the products of a step's spans; k: the lane's first column of the
-  // first span; xs: its first piece of the tokens there (row stride of a token
+  // acc += the products of a step's spans; left: columns of the slice from the
+  // lane's first on (WHOLE: both spans are there); xs: its first piece of the tokens there (row stride of a token
   // and part a.xrow); fac: the factors of the lane's two tokens there; xnext,
   // fnext: offsets of the second span's.
-  static __device__ __forceinline__ void step(const VecArgs& a, const Load (&v)[PAIR], int64_t k, int64_t kend,
-                                              const uint8_t* const (&xs)[NT], int xnext, const float* fac, int fnext,
-                                              bool plain, int lane, float (&acc)[NT][4]) {
+  template <bool WHOLE>
+  static __device__ __forceinline__ void step(const VecArgs& a, const Load (&v)[PAIR], int left, const uint8_t* const (&xs)[NT], int xnext, const float* fac, int fnext,
+                                              bool plain, int64_t kend, int lane, float (&acc)[NT][4]) {
     uint32_t mul[PAIR][2][BPL];
     bool odd = plain;
 #pragma unroll
-    for (int s = 0; s < PAIR; ++s) odd |= multipliers(v[s], k + s * SPAN, kend, mul[s]);
+    for (int s = 0; s < PAIR; ++s) odd |= multipliers<WHOLE>(v[s], left - s * SPAN, mul[s]);
     if (FMT == KRONQ_MXFP4 ? __any_sync(0xffffffffu, odd) : plain) {
 #pragma unroll
-      for (int s = 0; s < PAIR; ++s) scalar(a, v[s], k + s * SPAN, kend, lane, acc);
+      for (int s = 0; s < PAIR; ++s) scalar(a, v[s], kend - left + s * SPAN, kend, lane, acc);
       return;
     }
     float sum[PAIR][NT][PARTS][4] = {};
@@ -327,6 +342,7 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
   int* plain = reinterpret_cast<int*>(fac + spans * 8 * NT);
 
   // the copies' position: RING - 1 steps ahead of the arithmetic's
+  const int whole = cols / SPAN;                            // spans without a ragged end
   const int hop_k = wk * PAIR;                              // spans from a warp's step to its next
   int64_t ctile = (int64_t)blockIdx.x * wr + rw;
   int cspan = kw * PAIR;
@@ -335,7 +351,8 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
   const int row_left = (int)min(a.ldc * 2 - k0 - 32 * t, (int64_t)1 << 30);
   auto copy_next = [&]() {
     if (ctile < tiles && cspan < spans) {
-      V::copy(a, at, row_left - cspan * SPAN, (spans - cspan) * SPAN, cslot, lane);
+      if (cspan + PAIR <= whole) V::copy_whole(at, cslot, lane);
+      else V::copy(a, at, row_left - cspan * SPAN, (spans - cspan) * SPAN, cslot, lane);
       cspan += hop_k;
 #pragma unroll
       for (int h = 0; h < 2; ++h) at.c[h] += hop_k * (SPAN / 2);
@@ -397,7 +414,8 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
   for (int nt = 0; nt < NT; ++nt) xs[nt] = xpart + (int64_t)min(8 * nt + g, a.T - 1) * V::PARTS * a.xrow + 16 * t;
 
   const float wg = !a.part && a.wg ? *a.wg : 1.f;
-  int buf = 0, slot = 0;
+  int buf = 0;
+  const uint8_t* held = ring;
   for (int64_t tile0 = (int64_t)blockIdx.x * wr; tile0 < tiles; tile0 += hop, buf ^= 1) {
     float acc[NT][4] = {};
     if (tile0 + rw < tiles) {
@@ -406,17 +424,24 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
         asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
         __syncwarp();   // the other lanes' copies are in, and they are done with the slot that is copied to next
         copy_next();
-        // a second span beyond the last has zero weights: any tokens do
-        const int has = sp + 1 < spans ? 1 : 0;
         const uint8_t* xp[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) xp[nt] = xs[nt] + sp * 256;
         typename V::Load v[PAIR];
 #pragma unroll
-        for (int s = 0; s < PAIR; ++s) v[s] = V::take(ring + (slot * PAIR + s) * RSLOT, lane);
-        V::step(a, v, k0 + sp * SPAN + 32 * t, k0 + cols, xp, has * 256, fac + sp * 8 * NT + 2 * t, has * 8 * NT,
-                (plain[sp] | plain[sp + has]) != 0, lane, acc);
-        if (++slot == RING) slot = 0;
+        for (int s = 0; s < PAIR; ++s) v[s] = V::take(held + s * RSLOT, lane);
+        const float* fp = fac + sp * 8 * NT + 2 * t;
+        const int left = cols - sp * SPAN - 32 * t;
+        if (sp + PAIR <= whole) {
+          V::template step<true>(a, v, left, xp, 256, fp, 8 * NT, (plain[sp] | plain[sp + 1]) != 0, k0 + cols, lane, acc);
+        } else {
+          // a second span beyond the last has zero weights: any tokens do
+          const int has = sp + 1 < spans ? 1 : 0;
+          V::template step<false>(a, v, left, xp, has * 256, fp, has * 8 * NT, (plain[sp] | plain[sp + has]) != 0,
+                                  k0 + cols, lane, acc);
+        }
+        held += PAIR * RSLOT;
+        if (held == ring + RING * PAIR * RSLOT) held = ring;
       }
     }
     float* out = red[buf][warp];
