@@ -14,7 +14,7 @@
 // words with row r in lane r % 32, word r / 32.  The user's layout is row by
 // row, so loader warps read 16 bytes of four rows 32 apart, transpose
 // the 4 x 4 words in registers and store 16-byte rows of four such 512-byte
-// atoms; tcgen05.cp spreads an atom over TMEM, one chunk ahead of its MMAs.
+// atoms; tcgen05.cp spreads an atom over TMEM, one loader group ahead of its MMAs.
 // They work in groups of two such pieces (32 bytes of scales of a row), four
 // groups in flight in registers and two or four in shared memory, because a
 // load, its way to the barrier and the copy take longer than the MMAs of a few
@@ -60,7 +60,7 @@ constexpr int GROUP_INTS = 2 * (KRONQ_FP4_MAX_EXPERTS + 1);
 constexpr int LOADERS = 6, EPI = 8;           // warps
 constexpr int THREADS = 32 * (2 + LOADERS + EPI);
 constexpr int smem_bytes(int fmt) { return stages(fmt) * STAGE + slots(fmt) * SLOT + 256 + GROUP_INTS * 4 + 1024; }
-constexpr uint32_t SF_COL = GN;               // TMEM columns of the scales: 4 chunks of 48
+constexpr uint32_t SF_COL = GN;               // TMEM columns of the scales: two groups of 96
 
 struct GemmArgs {
   const uint8_t *xs, *ws;
@@ -167,11 +167,13 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)
       : "r"(taddr));
 }
 
-// A 512-byte scale atom to four TMEM columns; lo, hi: words of its descriptor.
-__device__ __forceinline__ void copy_atom(uint32_t tcol, uint32_t lo, uint32_t hi) {
+// A 512-byte scale atom to four TMEM columns, where `go` is not 0; lo, hi:
+// words of its descriptor.
+__device__ __forceinline__ void copy_atom(uint32_t tcol, uint32_t lo, uint32_t hi, uint32_t go) {
   asm volatile(
-      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\ttcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(tcol),
-      "r"(lo), "r"(hi)
+      "{\n\t.reg .b64 d;\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b64 d, {%1, %2};\n\t"
+      "@p tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(tcol),
+      "r"(lo), "r"(hi), "r"(go)
       : "memory");
 }
 
@@ -320,64 +322,80 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && elect_lane()) {
-      // Counters advance by increments and descriptors by adding to their low
-      // words: this thread's own instructions are as long as the MMAs.
+      // This thread's own instructions take about as long as the MMAs, so the
+      // loop runs over whole loader groups without a branch for each chunk,
+      // counters advance by increments and descriptors by adding to their low
+      // words.  A group's scales go to TMEM while the group before is
+      // multiplied, chunk by chunk, into the other of two buffers.
+      constexpr int CH = 2 * CPP;             // chunks of a group
+      constexpr uint32_t kCols = 48 / CPP;    // TMEM columns of a chunk's scales
       uint32_t s = 0, ph = 0;                 // stage of codes
       uint32_t slot = 0, sph = 0;             // slot of scales
-      uint32_t cbuf = 0, mbuf = 0;            // TMEM buffers: next copy's, next MMAs'
+      uint32_t buf = 0;                       // TMEM buffer of the group that is multiplied
       int done_tiles = 0;
       bool ok = true, issued = false;
-      const uint32_t stage0 = smem_u32(smem) >> 4, atom0 = (smem_u32(sfmem) >> 4) | (128u >> 4 << 16);
+      const uint32_t stage0 = (smem_u32(smem) >> 4) | (1u << 16);
+      const uint32_t atom0 = (smem_u32(sfmem) >> 4) | (128u >> 4 << 16);
       constexpr uint32_t kAtomHi = (128 >> 4) | (1u << 14);                 // no swizzle, 8-row groups of 128 bytes
       constexpr uint32_t kCodeHi = (1024 >> 4) | (1u << 14) | (2u << 29);   // 128-byte swizzle
-      // scales of the unit's local chunk lc into TMEM; a group's slot is free
-      // once its last copy has run
-      auto copy_scales = [&](int lc, bool last) -> bool {
-        const int in = lc & (2 * CPP - 1);
-        if (in == 0) {
-          if (!await(sffull0 + 8 * slot, sph, abort_s)) return false;
-          tc_fence_after();
-        }
-        const uint32_t atom = atom0 + slot * (SLOT >> 4) + (in / CPP) * (PIECE >> 4) + (CPP == 1 ? 0 : (in & 1) * 64);
-        const uint32_t sf = tmem + SF_COL + cbuf * 48;
-        const bool two = t.cols > GH;
+      // scales of chunk i of the group in `slot`
+      auto copy_scales = [&](int i, uint32_t to, uint32_t two) {
+        const uint32_t atom = atom0 + slot * (SLOT >> 4) + (i / CPP) * (PIECE >> 4) + (CPP == 1 ? 0 : (i & 1) * 64);
+        const uint32_t sf = tmem + SF_COL + to * 96 + i * kCols;
 #pragma unroll
         for (int j = 0; j < 4 / CPP; ++j) {
-          copy_atom(sf + 4 * j, atom + 32 * j, kAtomHi);
-          copy_atom(sf + 16 + 8 * j, atom + 128 + 32 * j, kAtomHi);
-          if (two) copy_atom(sf + 20 + 8 * j, atom + 256 + 32 * j, kAtomHi);
+          copy_atom(sf + 4 * j, atom + 32 * j, kAtomHi, 1u);
+          copy_atom(sf + kCols / 3 + 8 * j, atom + 128 + 32 * j, kAtomHi, 1u);
+          copy_atom(sf + kCols / 3 + 4 + 8 * j, atom + 256 + 32 * j, kAtomHi, two);
         }
-        issued = true;
-        if (in == 2 * CPP - 1 || last) {
-          mma_commit_pair_mc(sfempty0 + 8 * slot, 0x3);
-          if (++slot == SLOTS) { slot = 0; sph ^= 1; }
-        }
-        cbuf = (cbuf + 1) & 3;
-        return true;
+      };
+      auto scales_done = [&]() {
+        mma_commit_pair_mc(sfempty0 + 8 * slot, 0x3);
+        if (++slot == SLOTS) { slot = 0; sph ^= 1; }
       };
       for (int u = pair; ok && walk.get(a, u, t); u += npairs, ++done_tiles) {
         const int count = t.c1 - t.c0;
-        ok = copy_scales(0, count == 1);
-        if (ok && done_tiles > 0) ok = await(accempty, (done_tiles - 1) & 1, abort_s);
-        tc_fence_after();
+        const uint32_t two = t.cols > GH ? 1u : 0u;
         const uint32_t idesc = fp4_idesc<FMT>(t.cols, 0);
-        for (int lc = 0; ok && lc < count; ++lc) {
-          if (lc + 1 < count) ok = copy_scales(lc + 1, lc + 2 == count);
-          ok = ok && await(full0 + 8 * s, ph, abort_s);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sf = tmem + SF_COL + mbuf * 48;
-          const uint32_t wlo = (stage0 + s * (STAGE >> 4)) | (1u << 16);
+        ok = await(sffull0 + 8 * slot, sph, abort_s);
+        if (!ok) break;
+        tc_fence_after();
+        issued = true;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const int j = kk / CPP;
-            const uint32_t id = CPP == 1 ? 0u : 2u * (kk & 1);
-            mma_fp4_pair<FMT>(tmem, wlo + 2 * kk, wlo + (WBOX >> 4) + 2 * kk, kCodeHi, idesc | (id << 4) | (id << 29),
-                              sf + 4 * j, sf + 16 + 8 * j, (lc | kk) != 0 ? 1u : 0u);
+        for (int i = 0; i < CH; ++i) copy_scales(i, buf, two);
+        scales_done();
+        if (done_tiles > 0) ok = await(accempty, (done_tiles - 1) & 1, abort_s);
+        tc_fence_after();
+        for (int lc = 0; ok && lc < count; lc += CH) {
+          const bool more = lc + CH < count;
+          if (more) {
+            ok = await(sffull0 + 8 * slot, sph, abort_s);
+            if (!ok) break;
+            tc_fence_after();
           }
-          mma_commit_pair_mc(empty0 + 8 * s, 0x3);
-          mbuf = (mbuf + 1) & 3;
-          if (++s == STAGES) { s = 0; ph ^= 1; }
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            if (lc + i < count) {
+              if (more) copy_scales(i, buf ^ 1, two);
+              ok = ok && await(full0 + 8 * s, ph, abort_s);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t sf = tmem + SF_COL + buf * 96 + i * kCols;
+              const uint32_t wlo = stage0 + s * (STAGE >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const int j = kk / CPP;
+                const uint32_t id = CPP == 1 ? 0u : 2u * (kk & 1);
+                mma_fp4_pair<FMT>(tmem, wlo + 2 * kk, wlo + (WBOX >> 4) + 2 * kk, kCodeHi,
+                                  idesc | (id << 4) | (id << 29), sf + 4 * j, sf + kCols / 3 + 8 * j,
+                                  i + kk > 0 || lc > 0 ? 1u : 0u);
+              }
+              mma_commit_pair_mc(empty0 + 8 * s, 0x3);
+              if (++s == STAGES) { s = 0; ph ^= 1; }
+            }
+          }
+          if (ok && more) scales_done();
+          buf ^= 1;
         }
         if (ok) mma_commit_pair_mc(accfull, 0x3);
       }
