@@ -44,7 +44,8 @@ using namespace kq;
 extern "C" {
 
 size_t kronq_fp4_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n, kronq_fp4_format fmt) {
-  return 0;
+  if (!fp4_fmt_ok(fmt) || T <= 0 || T > kFp4MaxDim || m <= 0 || m > kFp4MaxDim || n <= 0 || n > kFp4MaxDim) return 0;
+  return fp4_gemm_workspace(T, m, n);
 }
 
 kronq_status kronq_fp4_matmul(const uint8_t* xc, const uint8_t* xs, const float* xg, const uint8_t* wc,
@@ -54,7 +55,10 @@ kronq_status kronq_fp4_matmul(const uint8_t* xc, const uint8_t* xs, const float*
   kronq_status r = check_product("fp4_matmul", fmt, T, m, n, xc, wc, ws, wg, y, ydt, ldy);
   if (r == KRONQ_OK) r = check_tokens("fp4_matmul", fmt, T, xc, xs, xg);
   if (r != KRONQ_OK || T == 0) return r;
-  Fp4Gemm g{xc, xs, xg, wc, ws, wg, T, m, n, y, ydt == KRONQ_BF16, ldy, nullptr, 1};
+  const size_t need = fp4_gemm_workspace(T, m, n);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+    return fail(KRONQ_ERR_INVALID_ARG, "fp4_matmul: workspace too small or not 256-byte aligned");
+  Fp4Gemm g{xc, xs, xg, wc, ws, wg, T, m, n, y, ydt == KRONQ_BF16, ldy, nullptr, 1, workspace};
   return fp4_gemm(g, fmt, as_stream(s));
 }
 
@@ -97,7 +101,7 @@ kronq_status kronq_fp4_grouped_matmul(const uint8_t* xc, const uint8_t* xs, cons
   if (!offsets) return fail(KRONQ_ERR_INVALID_ARG, "fp4_grouped_matmul: NULL pointer");
   if (!aligned(offsets, 4)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_grouped_matmul: misaligned pointer");
   if (T == 0) return KRONQ_OK;
-  Fp4Gemm g{xc, xs, xg, wc, ws, wg, T, m, n, y, ydt == KRONQ_BF16, ldy, offsets, E};
+  Fp4Gemm g{xc, xs, xg, wc, ws, wg, T, m, n, y, ydt == KRONQ_BF16, ldy, offsets, E, nullptr};
   return fp4_gemm(g, fmt, as_stream(s));
 }
 

@@ -158,15 +158,6 @@ __device__ void group_walk(const GemmArgs& a, int* bound, int* first, int lane) 
   if (lane == 0) first[a.E] = sum;
 }
 
-// 32 lanes x 16 consecutive 32-bit columns: thread t gets lane (base + t).
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr));
-}
-
 // A 512-byte scale atom to four TMEM columns, where `go` is not 0; lo, hi:
 // words of its descriptor.
 __device__ __forceinline__ void copy_atom(uint32_t tcol, uint32_t lo, uint32_t hi, uint32_t go) {
@@ -511,17 +502,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           if (g < groups) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(acc + (uint32_t)(2 * g + half) * 32, v);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t v[16];
-              tmem_ld_32x32b_x16(acc + (uint32_t)(2 * g + half) * 32 + 16 * c, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[2 * e]), xg), wg),
-                                                               __fmul_rn(__fmul_rn(__uint_as_float(v[2 * e + 1]), xg), wg));
-                pk[g][8 * c + e] = *reinterpret_cast<const uint32_t*>(&h);
-              }
+            for (int e = 0; e < 16; ++e) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[2 * e]), xg), wg),
+                                                             __fmul_rn(__fmul_rn(__uint_as_float(v[2 * e + 1]), xg), wg));
+              pk[g][e] = *reinterpret_cast<const uint32_t*>(&h);
             }
           }
         }
@@ -572,6 +560,32 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// y = the splits' partial sums in order, scaled.
+__global__ void __launch_bounds__(256) fp4_join_kernel(const GemmArgs a, int bf16) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = a.T * a.m;
+  if (i >= total) return;
+  float v = 0.f;
+  for (int s = 0; s < a.splits; ++s) v += a.part[s * total + i];
+  v = __fmul_rn(__fmul_rn(v, a.xg ? *a.xg : 1.f), a.wg ? *a.wg : 1.f);
+  const int64_t t = i / a.m, r = i - t * a.m;
+  if (bf16) static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + r] = __float2bfloat16_rn(v);
+  else static_cast<float*>(a.y)[t * a.ldy + r] = v;
+}
+
+// Chunks of a split.  The columns are split where the tiles would leave at
+// least half of the pairs of SMs idle, into as many parts as give each pair
+// at most one, of at least kSplitChunks chunks each (below that the launch
+// that joins them costs what the split saves).
+constexpr int64_t kSplitPairs = 74, kSplitChunks = 16;
+int64_t split_chunks(int64_t T, int64_t m, int64_t n) {
+  const int64_t chunks = ceil_div(n, CK), tiles = ceil_div(m, GM) * ceil_div(T, GN);
+  if (2 * tiles > kSplitPairs) return chunks;
+  int64_t parts = kSplitPairs / tiles;
+  if (parts > chunks / kSplitChunks) parts = chunks / kSplitChunks;
+  if (parts < 2) return chunks;
+  return ceil_div(ceil_div(chunks, parts), 4) * 4;   // whole loader groups
+}
+
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GemmArgs);
 
 // Most pairs of the kernel that run at once on the current device (a property
@@ -615,6 +629,11 @@ cudaError_t status_fetch_fp4(int* out, cudaStream_t s) {
   return e;
 }
 
+size_t fp4_gemm_workspace(int64_t T, int64_t m, int64_t n) {
+  const int64_t splits = ceil_div(ceil_div(n, CK), split_chunks(T, m, n));
+  return splits > 1 ? (size_t)(ceil_div(splits * T * m * 4, 256) * 256) : 0;
+}
+
 kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   const int64_t tiles_m = ceil_div(g.m, GM), tiles_t = ceil_div(g.T, GN) + (g.offsets ? g.E : 0);
   if (g.n > (int64_t(1) << 24)) return fail(KRONQ_ERR_UNSUPPORTED, "fp4 product: row too long");
@@ -635,15 +654,17 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   a.kb = (int)ceil_div(g.n, fp4_block(fmt));
   a.nchunks = (int)ceil_div(g.n, CK);
   a.tiles_m = (int)tiles_m;
-  a.splits = 1;
-  a.per_split = a.nchunks;
-  a.y = g.y; a.ldy = g.ldy; a.part = nullptr;
-  static const Kernel kernels[4] = {fp4_gemm_kernel<KRONQ_MXFP4, false, false>, fp4_gemm_kernel<KRONQ_MXFP4, true, false>,
-                                    fp4_gemm_kernel<KRONQ_NVFP4, false, false>, fp4_gemm_kernel<KRONQ_NVFP4, true, false>};
-  const int which = 2 * (fmt == KRONQ_NVFP4) + (g.y_bf16 ? 1 : 0);
+  a.per_split = g.offsets ? a.nchunks : (int)split_chunks(g.T, g.m, g.n);
+  a.splits = (int)ceil_div(a.nchunks, a.per_split);
+  a.y = g.y; a.ldy = g.ldy;
+  a.part = a.splits > 1 ? static_cast<float*>(g.workspace) : nullptr;
+  static const Kernel kernels[6] = {fp4_gemm_kernel<KRONQ_MXFP4, false, false>, fp4_gemm_kernel<KRONQ_MXFP4, true, false>,
+                                    fp4_gemm_kernel<KRONQ_MXFP4, false, true>, fp4_gemm_kernel<KRONQ_NVFP4, false, false>,
+                                    fp4_gemm_kernel<KRONQ_NVFP4, true, false>, fp4_gemm_kernel<KRONQ_NVFP4, false, true>};
+  const int which = 3 * (fmt == KRONQ_NVFP4) + (a.part ? 2 : g.y_bf16 ? 1 : 0);
   const int smem = smem_bytes(fmt), pairs = active_pairs(kernels[which], which, smem);
   if (pairs < 1) return fail(KRONQ_ERR_CUDA, "fp4 product: no pair of SMs can run the kernel");
-  const int64_t most = tiles_m * tiles_t;
+  const int64_t most = tiles_m * tiles_t * a.splits;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -659,6 +680,10 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[which], mw, mx, mxf, a);
   count_launch();
   if (e != cudaSuccess) return cuda_fail(e, "fp4_gemm_kernel");
+  if (a.part) {
+    fp4_join_kernel<<<(unsigned)ceil_div(g.T * g.m, 256), 256, 0, s>>>(a, g.y_bf16);
+    KQ_LAUNCH_CHECK("fp4_join_kernel");
+  }
   return KRONQ_OK;
 }
 

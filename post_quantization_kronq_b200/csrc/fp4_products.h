@@ -17,7 +17,9 @@ struct Fp4Gemm {
   int64_t ldy;
   const int* offsets;   // grouped: E + 1 bounds on the device, else NULL
   int64_t E;
+  void* workspace;      // plain: fp4_gemm_workspace bytes
 };
+size_t fp4_gemm_workspace(int64_t T, int64_t m, int64_t n);
 kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s);
 
 struct Fp4Matvec {
