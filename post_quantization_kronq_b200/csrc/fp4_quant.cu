@@ -17,11 +17,16 @@
 //   - the E4M3 scale is taken from a float32 quotient (off by at most one
 //     code) and corrected by the same comparison of amax with 6 g times the
 //     two neighbouring midpoints.
+// Large tensors work out per CTA, for every scale byte, the amax that reaches
+// it and a reciprocal that gives bf16's exact decisions by the conversion
+// instruction (checked at the borders; NvTable).
 //
 // One thread per 16 elements (8 bytes of codes, 32 or 64 bytes of input),
 // lane pairs share an MXFP4 block.  Bound by HBM: the input once (twice when
 // the tensor scale is computed), codes, scales and the optional dequantised
 // values once.
+#include <algorithm>
+
 #include "fp4.cuh"
 #include "internal.h"
 
@@ -29,63 +34,7 @@ namespace kq {
 namespace {
 
 constexpr int QT = 256;               // threads per block
-constexpr int MAX_PARTIALS = 1184;    // 8 blocks on each of 148 SMs
-
-// ---------------------------------------------------------------- amax
-// Largest finite |x| of a rows x n tensor as one partial per block (float
-// bits; non-negative floats order like their bits).
-__device__ __forceinline__ uint32_t finite_abs_bits(uint32_t bits) {
-  const uint32_t a = bits & 0x7FFFFFFFu;
-  return a < 0x7F800000u ? a : 0u;
-}
-
-template <bool BF16>
-__global__ void __launch_bounds__(QT)
-    fp4_amax_kernel(const void* x, int64_t rows, int64_t n, int64_t ldx, int vec, uint32_t* partial) {
-  uint32_t best = 0;
-  constexpr int E = BF16 ? 8 : 4;  // elements of a 16-byte load
-  const int64_t per = vec ? (n + E - 1) / E : n;
-  const int64_t total = rows * per;
-  const int64_t stride = (int64_t)gridDim.x * QT;
-  int64_t i = (int64_t)blockIdx.x * QT + threadIdx.x;
-  int64_t r = i / per, c = i - r * per;
-  const int64_t dr = stride / per, dc = stride - dr * per;
-#pragma unroll 4
-  for (; i < total; i += stride) {
-    if (vec && (c + 1) * E <= n) {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const char*>(x) + (r * ldx + c * E) * (BF16 ? 2 : 4));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (BF16) {
-          best = max(best, finite_abs_bits(u[q] << 16));
-          best = max(best, finite_abs_bits(u[q] & 0xFFFF0000u));
-        } else {
-          best = max(best, finite_abs_bits(u[q]));
-        }
-      }
-    } else {
-      const int64_t c0 = vec ? c * E : c, c1 = vec ? n : c + 1;
-      for (int64_t j = c0; j < c1; ++j) {
-        const int64_t at = r * ldx + j;
-        best = max(best, finite_abs_bits(BF16 ? (uint32_t)static_cast<const uint16_t*>(x)[at] << 16
-                                              : static_cast<const uint32_t*>(x)[at]));
-      }
-    }
-    r += dr;
-    c += dc;
-    if (c >= per) { c -= per; ++r; }
-  }
-  best = __reduce_max_sync(0xffffffffu, best);
-  __shared__ uint32_t red[QT / 32];
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = best;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 1; w < QT / 32; ++w) best = max(best, red[w]);
-    partial[blockIdx.x] = best;
-  }
-}
+constexpr int MAX_PARTIALS = 1024;    // partial maxima, at most one per block
 
 // ---------------------------------------------------------------- quantise
 struct QuantArgs {
@@ -100,6 +49,7 @@ struct QuantArgs {
   void* deq;              // dequantised values in x's type, or NULL
   int64_t ldd;
   int vec_in, vec_out;      // rows are 32-byte aligned
+  int table;                // NVFP4: borders and reciprocals of every scale are worked out first
   uintptr_t x_lo, x_hi;     // first byte of x, one behind its last
 };
 
@@ -152,6 +102,58 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// What NVFP4's rounding takes from a scale's byte, for all of them at once (a
+// CTA works out both in about a microsecond, which pays from two blocks a
+// thread on): the smallest amax that reaches the byte, and for bf16 input a
+// reciprocal r of scale g for which RN_e2m1(x r) in float32 is the exact
+// decision for every bf16 x.  RN_e2m1(x r) does not decrease in x, so it is
+// enough that it is right on both sides of the seven borders; 0 where none of
+// the neighbouring floats does that (the borders are compared then).  For
+// float32 input the reciprocal is just the rounded one: x r is off by at most
+// 3 units in its last place (three roundings of 2^-24 relative), and a block
+// with an x r within 8 units of a value of three significant bits, as the
+// borders are, compares with the borders.
+struct NvTable {
+  float reach[128];
+  float recip[128];
+};
+__device__ __forceinline__ uint32_t e2m1_code(float x) {
+  uint32_t b;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(b) : "f"(0.f), "f"(x));
+  return b & 15u;
+}
+template <bool BF16>
+__device__ __forceinline__ void fill_table(NvTable& tab, float g, int c) {
+  const float v = e4m3_value(min(c, 126));
+  if (c == 0) {
+    tab.reach[0] = 0.f;
+  } else if (c == 127) {
+    tab.reach[127] = __uint_as_float(0x7F800000u);
+  } else {   // a tie at an even byte's lower midpoint reaches it
+    const float mid = __fmul_rn(3.f, __fadd_rn(v, e4m3_value(c - 1)));
+    tab.reach[c] = (c & 1) ? __uint_as_float(__float_as_uint(__fmul_rd(mid, g)) + 1u) : __fmul_ru(mid, g);
+  }
+  if (BF16) {
+    float found = 0.f;
+    if (c > 0 && c < 127) {
+      const float r0 = __fdiv_rn(1.f, __fmul_rn(v, g));
+      for (int k = 0; k < 5 && found == 0.f; ++k) {   // r0, then one and two steps down and up
+        const float r = __uint_as_float(__float_as_uint(r0) + (k & 1 ? -((k + 1) >> 1) : k >> 1));
+        bool right = true;
+        for (int i = 0; i < 7; ++i) {
+          const uint32_t pass = pass_bf16x2(i, v, g) << 16;
+          right &= e2m1_code(__uint_as_float(pass) * r) > (uint32_t)i &&
+                   e2m1_code(__uint_as_float(pass - 0x10000u) * r) <= (uint32_t)i;
+        }
+        if (right) found = r;
+      }
+    }
+    tab.recip[c] = found;
+  } else {
+    tab.recip[c] = c > 0 && c < 127 ? __fdiv_rn(1.f, __fmul_rn(v, g)) : 0.f;
+  }
 }
 
 // 32-byte global loads and stores (whole sectors a lane).
@@ -277,10 +279,87 @@ __device__ __forceinline__ void values16(uint32_t lo, uint32_t hi, float s, floa
   }
 }
 
+// Largest magnitude of 16 elements; a NaN stays NaN.
+template <bool BF16>
+__device__ __forceinline__ float block_max(const uint32_t (&w)[BF16 ? 8 : 16]) {
+  if (BF16) {
+    __nv_bfloat162 m2 = __habs2(as_bf162(w[0]));
+#pragma unroll
+    for (int q = 1; q < 8; ++q) m2 = __hmax2_nan(m2, __habs2(as_bf162(w[q])));
+    const uint32_t u = as_u32(m2);
+    return max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
+  float m = fabsf(__uint_as_float(w[0]));
+#pragma unroll
+  for (int q = 1; q < 16; ++q) m = max_nan(m, fabsf(__uint_as_float(w[BF16 ? 0 : q])));
+  return m;
+}
+
+// Largest finite |x| as one partial per block (float bits; non-negative floats
+// order like their bits).  A warp takes AMAX_RUNS runs of 32 x 16 elements at
+// a time, so that their loads are in flight together.
+constexpr int AMAX_RUNS = 2;
+template <bool BF16>
+__global__ void __launch_bounds__(QT, 4) fp4_amax_kernel(const QuantArgs a, uint32_t* partial) {
+  constexpr int NW = BF16 ? 8 : 16;
+  constexpr int RUNS = BF16 ? 2 * AMAX_RUNS : AMAX_RUNS;
+  float best = 0.f;
+  const int64_t per = (a.n + 15) / 16, total = a.rows * per;
+  const int lane = threadIdx.x & 31;
+  const int64_t stride = (int64_t)gridDim.x * QT * RUNS;
+  const int64_t dr = stride / per, dc = stride - dr * per, ur = 32 / per, uc = 32 - ur * per;
+  int64_t base = (int64_t)blockIdx.x * QT * RUNS + (int64_t)(threadIdx.x >> 5) * 32 * RUNS;
+  int64_t r = (base + lane) / per, c = base + lane - r * per;
+  for (; base < total; base += stride) {
+    uint32_t w[RUNS][NW];
+    int64_t rr = r, cc = c;
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      if (base + 32 * k + lane < total) {
+        load16<BF16>(a, rr, cc * 16, w[k]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < NW; ++q) w[k][q] = 0u;
+      }
+      rr += ur;
+      cc += uc;
+      if (cc >= per) { cc -= per; ++rr; }
+    }
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      const float m = block_max<BF16>(w[k]);
+      if (m <= 3.40282347e38f) {
+        best = fmaxf(best, m);
+      } else {   // the block's finite values
+#pragma unroll
+        for (int q = 0; q < NW; ++q) {
+          const float hi = fabsf(__uint_as_float(BF16 ? w[k][q] & 0xFFFF0000u : w[k][q]));
+          const float lo = BF16 ? fabsf(__uint_as_float(w[k][q] << 16)) : 0.f;
+          if (hi <= 3.40282347e38f) best = fmaxf(best, hi);
+          if (lo <= 3.40282347e38f) best = fmaxf(best, lo);
+        }
+      }
+    }
+    r += dr;
+    c += dc;
+    if (c >= per) { c -= per; ++r; }
+  }
+  uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(best));
+  __shared__ uint32_t red[QT / 32];
+  if (lane == 0) red[threadIdx.x >> 5] = bits;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int q = 1; q < QT / 32; ++q) bits = max(bits, red[q]);
+    partial[blockIdx.x] = bits;
+  }
+}
+
 template <int FMT, bool BF16>
 __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) {
   __shared__ RunSmem runs[QT / 32];
-  float g = 1.f;
+  __shared__ NvTable tab;
+  float g = 1.f, inv6g = 0.f;
   bool g_bad = false;
   if (FMT == KRONQ_NVFP4) {
     if (a.partial) {
@@ -300,18 +379,29 @@ __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) 
       g_bad = !(g >= 1.17549435e-38f && g <= 3.40282347e38f);
     }
   }
+  // (the quotients stay normal for these g)
+  const bool table = FMT == KRONQ_NVFP4 && a.table && g >= 0x1p-100f && g <= 0x1p100f;
+  if (FMT == KRONQ_NVFP4 && table) {
+    inv6g = __fdiv_rn(1.f, __fmul_rn(6.f, g));
+    if (threadIdx.x < 128) fill_table<BF16>(tab, g, threadIdx.x);
+    __syncthreads();
+  }
   // units of 16 columns; the scale row's padding is covered too
   const int64_t per = a.lds * (FMT == KRONQ_MXFP4 ? 2 : 1);
   const int64_t total = a.rows * per;
   const int64_t stride = (int64_t)gridDim.x * QT;
   const int64_t first = (int64_t)blockIdx.x * QT;
-  int64_t i = first + threadIdx.x;
+  // from the last units to the first: what the pass for the tensor scale read
+  // last is still in L2
+  const int64_t warp0 = first + (threadIdx.x & ~31);
+  const int64_t steps = warp0 < total ? (total - warp0 + stride - 1) / stride : 0;
+  int64_t i = first + threadIdx.x + (steps - 1) * stride;
   int64_t r = i / per, c = i - r * per;
   const int64_t dr = stride / per, dc = stride - dr * per;
   // per is even for MXFP4, so a lane pair always holds one block; every warp
   // runs the same number of steps (total is a multiple of 16, lanes beyond it
   // only take part in the pair exchange)
-  for (int64_t base = first + (threadIdx.x & ~31); base < total; base += stride) {
+  for (int64_t n = 0; n < steps; ++n) {
     const bool live = i < total;
     const int64_t j0 = c * 16;
     uint32_t w[BF16 ? 8 : 16];
@@ -321,19 +411,7 @@ __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) 
 #pragma unroll
       for (int q = 0; q < (BF16 ? 8 : 16); ++q) w[q] = 0u;
     }
-    // block maximum; a NaN stays NaN
-    float amax;
-    if (BF16) {
-      __nv_bfloat162 m2 = __habs2(as_bf162(w[0]));
-#pragma unroll
-      for (int q = 1; q < 8; ++q) m2 = __hmax2_nan(m2, __habs2(as_bf162(w[q])));
-      const uint32_t u = as_u32(m2);
-      amax = max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-    } else {
-      amax = fabsf(__uint_as_float(w[0]));
-#pragma unroll
-      for (int q = 1; q < 16; ++q) amax = max_nan(amax, fabsf(__uint_as_float(w[BF16 ? 0 : q])));
-    }
+    float amax = block_max<BF16>(w);
     if (FMT == KRONQ_MXFP4) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     const bool bad = g_bad || !(amax <= 3.40282347e38f);
     uint32_t sbyte;
@@ -359,10 +437,49 @@ __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) 
         packed |= (uint64_t)b << (8 * q);
       }
     } else {
-      sbyte = bad ? 0x7Fu : nv_scale(amax, g);
+      if (bad) {
+        sbyte = 0x7Fu;
+      } else if (table) {   // a quotient that is off by one byte at most, then the exact borders
+        uint16_t p;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(0.f), "f"(amax * inv6g));
+        sbyte = min(p & 0xFFu, 126u);
+        if (amax < tab.reach[sbyte]) --sbyte;
+        else if (amax >= tab.reach[sbyte + 1]) ++sbyte;
+      } else {
+        sbyte = nv_scale(amax, g);
+      }
       const float s = e4m3_value(sbyte);
       const bool none = bad || sbyte == 0u;   // no border is passed
-      if (BF16) {
+      float recip = table && !bad ? tab.recip[sbyte] : 0.f;
+      if (!BF16) {
+        bool near = false;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const uint32_t y = __float_as_uint(__fmul_rn(__uint_as_float(w[BF16 ? 0 : q]), recip));
+          near |= ((y + 8u) & 0x1FFFFFu) <= 16u;
+        }
+        if (near) recip = 0.f;   // (zeros count as near: blocks with exact zeros are compared too)
+      }
+      if (!BF16 && recip != 0.f) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t b;
+          asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+              : "=r"(b)
+              : "f"(__fmul_rn(__uint_as_float(w[BF16 ? 0 : 2 * q + 1]), recip)),
+                "f"(__fmul_rn(__uint_as_float(w[BF16 ? 0 : 2 * q]), recip)));
+          packed |= (uint64_t)b << (8 * q);
+        }
+      } else if (BF16 && recip != 0.f) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t b;
+          asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+              : "=r"(b)
+              : "f"(__uint_as_float(w[q] & 0xFFFF0000u) * recip), "f"(__uint_as_float(w[q] << 16) * recip));
+          packed |= (uint64_t)b << (8 * q);
+        }
+      } else if (BF16) {
         uint32_t cnt[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) cnt[q] = 0x43004300u;   // 128: the count ends up in the low bits
@@ -410,10 +527,10 @@ __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) 
       const int count = live && j0 < a.n ? (int)min((int64_t)16, a.n - j0) : 0;
       store_runs<BF16>(a.deq, r * a.ldd + j0, count, a.vec_out, v, runs[threadIdx.x >> 5], threadIdx.x & 31);
     }
-    i += stride;
-    r += dr;
-    c += dc;
-    if (c >= per) { c -= per; ++r; }
+    i -= stride;
+    r -= dr;
+    c -= dc;
+    if (c < 0) { c += per; --r; }
   }
 }
 
@@ -480,7 +597,7 @@ __global__ void __launch_bounds__(QT) fp4_dequantize_kernel(const DequantArgs a)
 // Blocks for `total` units of one thread each: at most as many as run at once
 // (per_sm: the kernel's registers allow that many).
 unsigned quant_grid(int64_t total, int per_sm) {
-  const int64_t want = ceil_div(total, QT), cap = per_sm * (int64_t)sm_count();
+  const int64_t want = ceil_div(total, QT), cap = std::min<int64_t>(per_sm * (int64_t)sm_count(), MAX_PARTIALS);
   return (unsigned)(want < 1 ? 1 : want < cap ? want : cap);
 }
 
@@ -540,16 +657,16 @@ kronq_status kronq_fp4_quantize(const void* x, kronq_dtype dt, int64_t rows, int
     uint32_t* partial = rows > 0 ? static_cast<uint32_t*>(workspace) : reinterpret_cast<uint32_t*>(gscale);
     a.partial = partial;
     if (rows > 0) {
-      const int64_t units = rows * (a.vec_in ? ceil_div(n, 16 / esize) : n);
-      unsigned grid = quant_grid(ceil_div(units, 4), 6);   // four loads in flight a thread
-      if (grid > (unsigned)MAX_PARTIALS) grid = MAX_PARTIALS;
-      if (dt == KRONQ_BF16) fp4_amax_kernel<true><<<grid, QT, 0, st>>>(x, rows, n, ldx, a.vec_in, partial);
-      else fp4_amax_kernel<false><<<grid, QT, 0, st>>>(x, rows, n, ldx, a.vec_in, partial);
+      const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), dt == KRONQ_BF16 ? 2 * AMAX_RUNS : AMAX_RUNS), 4);
+      if (dt == KRONQ_BF16) fp4_amax_kernel<true><<<grid, QT, 0, st>>>(a, partial);
+      else fp4_amax_kernel<false><<<grid, QT, 0, st>>>(a, partial);
       KQ_LAUNCH_CHECK("fp4_amax_kernel");
       a.npartial = (int)grid;
     }
   }
-  const unsigned grid = quant_grid(rows * a.lds * (fmt == KRONQ_MXFP4 ? 2 : 1), 4);
+  const int64_t units = rows * a.lds * (fmt == KRONQ_MXFP4 ? 2 : 1);
+  const unsigned grid = quant_grid(units, 4);
+  a.table = units >= 2 * (int64_t)grid * QT;
   if (fmt == KRONQ_MXFP4) {
     if (dt == KRONQ_BF16) fp4_quantize_kernel<KRONQ_MXFP4, true><<<grid, QT, 0, st>>>(a);
     else fp4_quantize_kernel<KRONQ_MXFP4, false><<<grid, QT, 0, st>>>(a);

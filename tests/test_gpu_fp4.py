@@ -92,6 +92,29 @@ def test_nv_borders_are_exact(dt, g):
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("g", [None, 1.0, 2.0 ** -9, 0.0123, 2.0 ** 100, 2.0 ** -100, 3e38, 2.0 ** -126, 1.7e-7])
+def test_nv_borders_are_exact_in_a_large_tensor(dt, g):
+    # as above with more than two blocks a thread, for every scale byte; a
+    # ragged last block; a row of NaN, a row of zeros
+    rng = np.random.default_rng(6)
+    rows, n = 20000, 250
+    gv = np.float32(0.31 if g is None else g)
+    table = fp4.e4m3_table()
+    s = table[(np.arange(rows) % 126 + 1)][:, None]
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])[rng.integers(0, 8, size=(rows, n))]
+    with np.errstate(over="ignore"):
+        x = np.clip(mids * s * np.float64(gv), 0, 3e38).astype(np.float32)
+        smid = np.clip((table[1:] + table[:-1]) / 2 * 6 * np.float64(gv), 0, 3e38).astype(np.float32)
+    x[:, 16:32] *= 0.25
+    x[:, 20] = smid[rng.integers(0, 126, size=rows)]
+    step = rng.integers(-1, 2, size=x.shape)
+    x = np.where(step < 0, np.nextafter(x, np.float32(0)), np.where(step > 0, np.nextafter(x, np.float32(3e38)), x))
+    x *= rng.choice(np.array([-1, 1], np.float32), size=x.shape)
+    x[7], x[9], x[11, 40] = np.nan, 0.0, np.inf
+    check_quantize(torch.from_numpy(x).to(dt).to(DEV), NV, None if g is None else gv)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_mx_borders_and_extreme_exponents(dt):
     rng = np.random.default_rng(4)
     e = rng.integers(-149, 128, size=(2048, 1)).astype(np.float64)
