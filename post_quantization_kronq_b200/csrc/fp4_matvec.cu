@@ -526,9 +526,14 @@ kronq_status fp4_matvec(const Fp4Matvec& v, int fmt, cudaStream_t st) {
   a.vec = aligned(v.x, 4 * esize) && v.ldx % 4 == 0;
   a.y = v.y; a.y_bf16 = v.y_bf16; a.ldy = v.ldy;
   a.part = slices > 1 ? static_cast<float*>(v.workspace) : nullptr;
+  // Warps along the columns: all eight, unless that leaves a warp fewer than
+  // four steps of a row tile between two joins of the warps' sums and there are
+  // rows enough to keep two rounds of CTAs busy.
+  const int64_t pairs = ceil_div(kslice, SPAN * PAIR), tiles = ceil_div(v.m, 16);
   a.wk = VW;
-  while (a.wk > 1 && a.wk * PAIR > ceil_div(kslice, SPAN * PAIR) * PAIR) a.wk /= 2;
-  const int64_t groups = ceil_div(ceil_div(v.m, 16), VW / a.wk);   // row tiles that a CTA takes at once
+  while (a.wk > 1 && (a.wk > pairs || (pairs < 4 * a.wk && tiles * (a.wk / 2) / VW * slices >= 2 * CTAS * 148)))
+    a.wk /= 2;
+  const int64_t groups = ceil_div(tiles, VW / a.wk);   // row tiles that a CTA takes at once
   int64_t gx = CTAS * (int64_t)sm_count() / slices;
   if (gx < 1) gx = 1;
   if (gx > groups) gx = groups;

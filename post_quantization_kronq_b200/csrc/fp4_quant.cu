@@ -219,49 +219,74 @@ __device__ __forceinline__ void load16(const QuantArgs& a, int64_t r, int64_t j0
 
 // A warp's 32 runs of up to 16 values, each to its place in a row: `at` the
 // element offset, `count` the elements (0 for a lane without any).  Aligned
-// rows take 32-byte stores.  Others go through shared memory, so that a store
-// instruction writes two runs' neighbouring elements, not one of each lane's.
-struct RunSmem {
-  float v[32 * 17];
-  int64_t at[32];
-  int count[32];
-};
+// rows take 32-byte stores.  In others a lane's stores are the 16-byte words
+// of memory that end in its run: it takes what the first of them needs from
+// the lane before, where that holds the run before in the row.  Elements that
+// no such word covers are stored one by one.
 template <bool BF16>
-__device__ __forceinline__ void store_runs(void* out, int64_t at, int count, bool vec, const float (&v)[16], RunSmem& sm,
-                                           int lane) {
-  const bool whole = vec && count == 16;
+__device__ __forceinline__ void store_runs(void* out, int64_t at, int count, bool vec, const float (&v)[16], int lane) {
+  constexpr int NW = BF16 ? 8 : 16, ES = BF16 ? 2 : 4;
+  uint32_t c[NW + 5];   // the four words before the run, the run
+#pragma unroll
+  for (int q = 0; q < NW; ++q)
+    c[4 + q] = BF16 ? as_u32(__floats2bfloat162_rn(v[2 * (q % 8)], v[2 * (q % 8) + 1])) : __float_as_uint(v[q]);
+  const uintptr_t addr = reinterpret_cast<uintptr_t>(out) + at * ES;
+  bool whole = count == 16;
+  if (vec && whole) {
+    store32(reinterpret_cast<void*>(addr), c + 4);
+    if (!BF16) store32(reinterpret_cast<void*>(addr + 32), c + (BF16 ? 4 : 12));
+  }
+  if (__all_sync(0xffffffffu, (vec && whole) || count == 0)) return;
+  if (vec && whole) count = 0, whole = false;
+  const uintptr_t before = __shfl_up_sync(0xffffffffu, (unsigned long long)addr, 1);
+  const int before_whole = __shfl_up_sync(0xffffffffu, (int)whole, 1);
+  const bool joins = lane > 0 && whole && before_whole && before + NW * 4 == addr;
+  const int next_joins = __shfl_down_sync(0xffffffffu, (int)joins, 1);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) c[q] = __shfl_up_sync(0xffffffffu, c[NW + q], 1);
+  c[NW + 4] = 0;
+  const int off = (int)(addr & 15);
+  int lo = 0, hi = count;      // elements stored one by one: up to lo, and from hi on
   if (whole) {
+    uint32_t w[NW + 5];
+#pragma unroll
+    for (int q = 0; q < NW + 5; ++q) w[q] = c[q];
+    // the words begin 16 - off bytes into c
+    const int skip = 16 - off;
+    if (skip & 16) {
+#pragma unroll
+      for (int q = 0; q < NW + 1; ++q) w[q] = w[q + 4];
+    }
+    if (skip & 8) {
+#pragma unroll
+      for (int q = 0; q < NW + 3; ++q) w[q] = w[q + 2];
+    }
+    if (skip & 4) {
+#pragma unroll
+      for (int q = 0; q < NW + 1; ++q) w[q] = w[q + 1];
+    }
     if (BF16) {
-      uint32_t u[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) u[q] = as_u32(__floats2bfloat162_rn(v[2 * q], v[2 * q + 1]));
-      store32(static_cast<__nv_bfloat16*>(out) + at, u);
-    } else {
-      uint32_t u[16];
+      for (int q = 0; q < NW; ++q) w[q] = __funnelshift_r(w[q], w[q + 1], 8 * (skip & 2));
+    }
+    uint4* o = reinterpret_cast<uint4*>(addr - off);
+    const bool head = off == 0 || joins;
+    if (head) o[0] = make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(v[q]);
-      store32(static_cast<float*>(out) + at, u);
-      store32(static_cast<float*>(out) + at + 8, u + 8);
+    for (int q = 1; q < NW / 4; ++q) o[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    lo = head ? 0 : skip / ES;
+    hi = next_joins && lane < 31 ? 16 : 16 - off / ES;
+    count = 16;
+  } else {
+    hi = 0;
+  }
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    if (q < count && (q < lo || q >= hi)) {
+      if (BF16) reinterpret_cast<__nv_bfloat16*>(addr)[q] = __float2bfloat16_rn(v[q]);
+      else reinterpret_cast<float*>(addr)[q] = v[q];
     }
   }
-  if (__all_sync(0xffffffffu, whole || count == 0)) return;
-  __syncwarp();
-#pragma unroll
-  for (int q = 0; q < 16; ++q) sm.v[lane * 17 + q] = v[q];
-  sm.at[lane] = at;
-  sm.count[lane] = whole ? 0 : count;
-  __syncwarp();
-  const int e = lane & 15;
-#pragma unroll 4
-  for (int k = 0; k < 16; ++k) {
-    const int u = 2 * k + (lane >> 4);
-    if (e < sm.count[u]) {
-      const float f = sm.v[u * 17 + e];
-      if (BF16) static_cast<__nv_bfloat16*>(out)[sm.at[u] + e] = __float2bfloat16_rn(f);
-      else static_cast<float*>(out)[sm.at[u] + e] = f;
-    }
-  }
-  __syncwarp();
 }
 
 // Values of 16 codes under a scale (and the tensor scale), with float32's roundings.
@@ -357,7 +382,6 @@ __global__ void __launch_bounds__(QT, 4) fp4_amax_kernel(const QuantArgs a, uint
 
 template <int FMT, bool BF16>
 __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) {
-  __shared__ RunSmem runs[QT / 32];
   __shared__ NvTable tab;
   float g = 1.f, inv6g = 0.f;
   bool g_bad = false;
@@ -525,7 +549,7 @@ __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) 
       float v[16];
       values16<FMT>((uint32_t)packed, (uint32_t)(packed >> 32), fp4_scale_value<FMT>(sbyte), g, v);
       const int count = live && j0 < a.n ? (int)min((int64_t)16, a.n - j0) : 0;
-      store_runs<BF16>(a.deq, r * a.ldd + j0, count, a.vec_out, v, runs[threadIdx.x >> 5], threadIdx.x & 31);
+      store_runs<BF16>(a.deq, r * a.ldd + j0, count, a.vec_out, v, threadIdx.x & 31);
     }
     i -= stride;
     r -= dr;
@@ -550,8 +574,7 @@ struct DequantArgs {
 constexpr int UNROLL = 4;
 
 template <int FMT, bool BF16>
-__global__ void __launch_bounds__(QT) fp4_dequantize_kernel(const DequantArgs a) {
-  __shared__ RunSmem runs[QT / 32];
+__global__ void __launch_bounds__(QT, 3) fp4_dequantize_kernel(const DequantArgs a) {
   const float g = FMT == KRONQ_NVFP4 ? *a.gscale : 1.f;
   const int64_t per = (a.n + 15) / 16;
   const int64_t total = a.rows * per;
@@ -586,7 +609,7 @@ __global__ void __launch_bounds__(QT) fp4_dequantize_kernel(const DequantArgs a)
     for (int k = 0; k < UNROLL; ++k) {
       float v[16];
       values16<FMT>(w[k].x, w[k].y, fp4_scale_value<FMT>(sb[k]), g, v);
-      store_runs<BF16>(a.out, at[k], count[k], a.vec_out, v, runs[threadIdx.x >> 5], lane);
+      store_runs<BF16>(a.out, at[k], count[k], a.vec_out, v, lane);
     }
     r += dr;
     c += dc;
