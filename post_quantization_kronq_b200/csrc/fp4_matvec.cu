@@ -370,41 +370,43 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
 #pragma unroll 1
   for (int i = 0; i < RING - 1; ++i) copy_next();
 
-  // a warp per span, four tokens' loads in flight
-  for (int sp = warp; sp < spans; sp += VW) {
-    const int k = sp * SPAN + 4 * lane;
-    uint8_t* dst = xpart + x_offset(k);
-    bool covered = true;
-    for (int tk0 = 0; tk0 < a.T; tk0 += 4) {
-      float f[4][4];
+  for (int i = threadIdx.x; i < spans * (8 * NT + 1); i += VT) fac[i] = 0.f;   // and plain
+  __syncthreads();
+  // a warp per span and token, four of them in flight
+  for (int u0 = warp; u0 < spans * a.T; u0 += 4 * VW) {
+    float f[4][4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int64_t src = (int64_t)min(tk0 + w, a.T - 1) * a.ldx + k0 + k;
-        if (a.vec && k + 4 <= cols) {
-          if (XF32) {
-            const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + src);
-            f[w][0] = q.x; f[w][1] = q.y; f[w][2] = q.z; f[w][3] = q.w;
-          } else {
-            const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + src);
-            f[w][0] = __uint_as_float(q.x << 16); f[w][1] = __uint_as_float(q.x & 0xFFFF0000u);
-            f[w][2] = __uint_as_float(q.y << 16); f[w][3] = __uint_as_float(q.y & 0xFFFF0000u);
-          }
+    for (int w = 0; w < 4; ++w) {
+      const int u = min(u0 + w * VW, spans * a.T - 1), sp = u / a.T;
+      const int k = sp * SPAN + 4 * lane;
+      const int64_t src = (u - sp * a.T) * a.ldx + k0 + k;
+      if (a.vec && k + 4 <= cols) {
+        if (XF32) {
+          const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + src);
+          f[w][0] = q.x; f[w][1] = q.y; f[w][2] = q.z; f[w][3] = q.w;
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) f[w][c] = k + c < cols ? x_at(a, XF32, src + c) : 0.f;
+          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.x) + src);
+          f[w][0] = __uint_as_float(q.x << 16); f[w][1] = __uint_as_float(q.x & 0xFFFF0000u);
+          f[w][2] = __uint_as_float(q.y << 16); f[w][3] = __uint_as_float(q.y & 0xFFFF0000u);
         }
-      }
+      } else {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if (tk0 + w < a.T) {
-          float factor;
-          covered &= stage_span<FMT, XF32>(f[w], dst + (int64_t)(tk0 + w) * V::PARTS * a.xrow, a.xrow, factor);
-          if (lane == 0) fac[sp * 8 * NT + tk0 + w] = factor;
+        for (int c = 0; c < 4; ++c) f[w][c] = k + c < cols ? x_at(a, XF32, src + c) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int u = u0 + w * VW, sp = u / a.T, tk = u - sp * a.T;
+      if (u < spans * a.T) {
+        float factor;
+        const bool covered = stage_span<FMT, XF32>(
+            f[w], xpart + (int64_t)tk * V::PARTS * a.xrow + x_offset(sp * SPAN + 4 * lane), a.xrow, factor);
+        if (lane == 0) {
+          fac[sp * 8 * NT + tk] = factor;
+          if (!covered) plain[sp] = 1;
         }
       }
     }
-    if (lane >= a.T && lane < 8 * NT) fac[sp * 8 * NT + lane] = 0.f;
-    if (lane == 0) plain[sp] = !covered;
   }
   __syncthreads();
 

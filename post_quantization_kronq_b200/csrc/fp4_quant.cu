@@ -223,21 +223,30 @@ __device__ __forceinline__ void load16(const QuantArgs& a, int64_t r, int64_t j0
 // of memory that end in its run: it takes what the first of them needs from
 // the lane before, where that holds the run before in the row.  Elements that
 // no such word covers are stored one by one.
-template <bool BF16>
-__device__ __forceinline__ void store_runs(void* out, int64_t at, int count, bool vec, const float (&v)[16], int lane) {
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store_runs(void* out, int64_t at, int count, const float (&v)[16], int lane) {
   constexpr int NW = BF16 ? 8 : 16, ES = BF16 ? 2 : 4;
   uint32_t c[NW + 5];   // the four words before the run, the run
 #pragma unroll
   for (int q = 0; q < NW; ++q)
     c[4 + q] = BF16 ? as_u32(__floats2bfloat162_rn(v[2 * (q % 8)], v[2 * (q % 8) + 1])) : __float_as_uint(v[q]);
   const uintptr_t addr = reinterpret_cast<uintptr_t>(out) + at * ES;
-  bool whole = count == 16;
-  if (vec && whole) {
-    store32(reinterpret_cast<void*>(addr), c + 4);
-    if (!BF16) store32(reinterpret_cast<void*>(addr + 32), c + (BF16 ? 4 : 12));
+  const bool whole = count == 16;
+  if (VEC) {
+    if (whole) {
+      store32(reinterpret_cast<void*>(addr), c + 4);
+      if (!BF16) store32(reinterpret_cast<void*>(addr + 32), c + (BF16 ? 4 : 12));
+    } else if (count > 0) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        if (q < count) {
+          if (BF16) reinterpret_cast<__nv_bfloat16*>(addr)[q] = __float2bfloat16_rn(v[q]);
+          else reinterpret_cast<float*>(addr)[q] = v[q];
+        }
+      }
+    }
+    return;
   }
-  if (__all_sync(0xffffffffu, (vec && whole) || count == 0)) return;
-  if (vec && whole) count = 0, whole = false;
   const uintptr_t before = __shfl_up_sync(0xffffffffu, (unsigned long long)addr, 1);
   const int before_whole = __shfl_up_sync(0xffffffffu, (int)whole, 1);
   const bool joins = lane > 0 && whole && before_whole && before + NW * 4 == addr;
@@ -549,7 +558,8 @@ __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) 
       float v[16];
       values16<FMT>((uint32_t)packed, (uint32_t)(packed >> 32), fp4_scale_value<FMT>(sbyte), g, v);
       const int count = live && j0 < a.n ? (int)min((int64_t)16, a.n - j0) : 0;
-      store_runs<BF16>(a.deq, r * a.ldd + j0, count, a.vec_out, v, threadIdx.x & 31);
+      if (a.vec_out) store_runs<BF16, true>(a.deq, r * a.ldd + j0, count, v, threadIdx.x & 31);
+      else store_runs<BF16, false>(a.deq, r * a.ldd + j0, count, v, threadIdx.x & 31);
     }
     i -= stride;
     r -= dr;
@@ -566,14 +576,13 @@ struct DequantArgs {
   const float* gscale;
   void* out;
   int64_t ldo;
-  int vec_out;
 };
 
 // Each warp step takes UNROLL runs of 16 codes a lane, so that enough loads
 // are in flight: a run reads only 9 bytes for the 32 or 64 that it writes.
 constexpr int UNROLL = 4;
 
-template <int FMT, bool BF16>
+template <int FMT, bool BF16, bool VEC>
 __global__ void __launch_bounds__(QT, 3) fp4_dequantize_kernel(const DequantArgs a) {
   const float g = FMT == KRONQ_NVFP4 ? *a.gscale : 1.f;
   const int64_t per = (a.n + 15) / 16;
@@ -609,7 +618,7 @@ __global__ void __launch_bounds__(QT, 3) fp4_dequantize_kernel(const DequantArgs
     for (int k = 0; k < UNROLL; ++k) {
       float v[16];
       values16<FMT>(w[k].x, w[k].y, fp4_scale_value<FMT>(sb[k]), g, v);
-      store_runs<BF16>(a.out, at[k], count[k], a.vec_out, v, lane);
+      store_runs<BF16, VEC>(a.out, at[k], count[k], v, lane);
     }
     r += dr;
     c += dc;
@@ -720,16 +729,16 @@ kronq_status kronq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, c
   a.codes = codes; a.scales = scales; a.rows = rows; a.n = n;
   a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
   a.gscale = gscale; a.out = out; a.ldo = ldo;
-  a.vec_out = aligned(out, 32) && (ldo * esize) % 32 == 0;
+  const int vec_out = aligned(out, 32) && (ldo * esize) % 32 == 0;   // rows are 32-byte aligned
   const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), UNROLL), 3);
   cudaStream_t st = as_stream(s);
-  if (fmt == KRONQ_MXFP4) {
-    if (dt == KRONQ_BF16) fp4_dequantize_kernel<KRONQ_MXFP4, true><<<grid, QT, 0, st>>>(a);
-    else fp4_dequantize_kernel<KRONQ_MXFP4, false><<<grid, QT, 0, st>>>(a);
-  } else {
-    if (dt == KRONQ_BF16) fp4_dequantize_kernel<KRONQ_NVFP4, true><<<grid, QT, 0, st>>>(a);
-    else fp4_dequantize_kernel<KRONQ_NVFP4, false><<<grid, QT, 0, st>>>(a);
-  }
+  using K = void (*)(const DequantArgs);
+  static const K kernels[8] = {
+      fp4_dequantize_kernel<KRONQ_MXFP4, false, false>, fp4_dequantize_kernel<KRONQ_MXFP4, false, true>,
+      fp4_dequantize_kernel<KRONQ_MXFP4, true, false>,  fp4_dequantize_kernel<KRONQ_MXFP4, true, true>,
+      fp4_dequantize_kernel<KRONQ_NVFP4, false, false>, fp4_dequantize_kernel<KRONQ_NVFP4, false, true>,
+      fp4_dequantize_kernel<KRONQ_NVFP4, true, false>,  fp4_dequantize_kernel<KRONQ_NVFP4, true, true>};
+  kernels[4 * (fmt == KRONQ_NVFP4) + 2 * (dt == KRONQ_BF16) + vec_out]<<<grid, QT, 0, st>>>(a);
   KQ_LAUNCH_CHECK("fp4_dequantize_kernel");
   return KRONQ_OK;
 }
