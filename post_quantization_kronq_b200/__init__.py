@@ -359,7 +359,8 @@ def _fp4_matrix(t, name):
     ld, one = t.stride()
     if one != 1 and n > 1:
         raise ValueError(f"{name} must have unit stride along its rows")
-    return t.data_ptr(), rows, n, ld if rows > 1 and ld > 0 else max(ld, n)
+    # a single row may carry any stride: pass one that keeps its alignment
+    return t.data_ptr(), rows, n, ld if rows > 1 else (n + 15) & ~15
 
 
 def _fp4_pair(codes, scales, name, fmt, lead, n, device):

@@ -23,9 +23,22 @@ inline int fp4_block(int fmt) { return fmt == KRONQ_MXFP4 ? 32 : 16; }
 inline int64_t fp4_code_row(int64_t n) { return ceil_div(ceil_div(n, 2), 16) * 16; }
 inline int64_t fp4_scale_row(int fmt, int64_t n) { return ceil_div(ceil_div(n, fp4_block(fmt)), 16) * 16; }
 
-// Largest row and column counts of the 4-bit calls: coordinates of the
-// tensor maps and tile indices are 32-bit.
+// Largest row and column counts of the 4-bit calls (coordinates of the tensor
+// maps and tile indices are 32-bit), and the largest row stride (offsets stay
+// within 64 bits).
 constexpr int64_t kFp4MaxDim = int64_t(1) << 30;
+constexpr int64_t kFp4MaxStride = int64_t(1) << 32;
+
+// Runs a C entry point's body; no exception (out of host memory, in building
+// an error message) passes the C boundary.
+template <typename F>
+kronq_status fp4_entry(F body) {
+  try {
+    return body();
+  } catch (...) {
+    return KRONQ_ERR_CUDA;
+  }
+}
 
 // Value of an E8M0 byte (255 is NaN) and of an E4M3 byte (0x7F is NaN).
 __device__ __forceinline__ float e8m0_value(uint32_t b) {

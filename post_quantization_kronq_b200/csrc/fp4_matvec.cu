@@ -501,7 +501,8 @@ int64_t slice_columns(int64_t T, int64_t m, int64_t n, bool x_f32) {
 template <int FMT, bool XF32>
 kronq_status launch_vec(const VecArgs& a, dim3 grid, int smem, cudaStream_t st) {
   void (*fn)(const VecArgs) = a.T > 8 ? fp4_matvec_kernel<FMT, XF32, 2> : fp4_matvec_kernel<FMT, XF32, 1>;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), smem);
+  // one limit for every call, so that calls of other threads do not lower it
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), RBYTES + XSMEM + 4 * 1024);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fp4 matvec)");
   fn<<<grid, VT, smem, st>>>(a);
   KQ_LAUNCH_CHECK("fp4_matvec_kernel");

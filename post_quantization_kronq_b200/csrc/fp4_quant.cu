@@ -655,92 +655,97 @@ kronq_status kronq_fp4_quantize(const void* x, kronq_dtype dt, int64_t rows, int
                                 kronq_fp4_format fmt, uint8_t* codes, uint8_t* scales, float* gscale,
                                 int gscale_given, void* deq, int64_t ldd, void* workspace, size_t ws_bytes,
                                 kronq_stream_t s) {
-  if (!fp4_fmt_ok(fmt)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: bad format");
-  if (dt != KRONQ_BF16 && dt != KRONQ_F32) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: bad dtype");
-  if (rows < 0 || rows > kFp4MaxDim || n <= 0 || n > kFp4MaxDim)
-    return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: sizes out of range");
-  if (ldx < n || (deq && ldd < n)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: row stride below n");
-  if (rows > 0 && (!x || !codes || !scales)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: NULL pointer");
-  if (fmt == KRONQ_NVFP4 && !gscale) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: NVFP4 needs gscale");
-  if (fmt == KRONQ_MXFP4 && gscale) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: MXFP4 has no tensor scale");
-  if (!aligned(codes, 16) || !aligned(scales, 16))
-    return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: codes and scales must be 16-byte aligned");
-  const int esize = dt == KRONQ_BF16 ? 2 : 4;
-  if (!aligned(x, esize) || (deq && !aligned(deq, esize)) || (gscale && !aligned(gscale, 4)))
-    return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: misaligned pointer");
-  const bool compute = fmt == KRONQ_NVFP4 && !gscale_given;
-  if (compute && rows > 0 &&
-      (!workspace || ws_bytes < kronq_fp4_quantize_workspace_bytes(rows, n, fmt) || !aligned(workspace, 256)))
-    return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: workspace too small or not 256-byte aligned");
-  if (rows == 0 && !compute) return KRONQ_OK;
-  cudaStream_t st = as_stream(s);
-  QuantArgs a;
-  a.x = x; a.rows = rows; a.n = n; a.ldx = ldx;
-  a.codes = codes; a.scales = scales;
-  a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
-  a.gscale = gscale;
-  a.partial = nullptr; a.npartial = 0;
-  a.deq = deq; a.ldd = ldd;
-  a.vec_in = aligned(x, 32) && (ldx * esize) % 32 == 0;
-  a.vec_out = deq && aligned(deq, 32) && (ldd * esize) % 32 == 0;
-  a.x_lo = reinterpret_cast<uintptr_t>(x);
-  a.x_hi = a.x_lo + (size_t)(rows > 0 ? (rows - 1) * ldx + n : 0) * esize;
-  if (compute) {
-    uint32_t* partial = rows > 0 ? static_cast<uint32_t*>(workspace) : reinterpret_cast<uint32_t*>(gscale);
-    a.partial = partial;
-    if (rows > 0) {
-      const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), dt == KRONQ_BF16 ? 2 * AMAX_RUNS : AMAX_RUNS), 4);
-      if (dt == KRONQ_BF16) fp4_amax_kernel<true><<<grid, QT, 0, st>>>(a, partial);
-      else fp4_amax_kernel<false><<<grid, QT, 0, st>>>(a, partial);
-      KQ_LAUNCH_CHECK("fp4_amax_kernel");
-      a.npartial = (int)grid;
+  return fp4_entry([&]() -> kronq_status {
+    if (!fp4_fmt_ok(fmt)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: bad format");
+    if (dt != KRONQ_BF16 && dt != KRONQ_F32) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: bad dtype");
+    if (rows < 0 || rows > kFp4MaxDim || n <= 0 || n > kFp4MaxDim)
+      return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: sizes out of range");
+    if (ldx < n || ldx > kFp4MaxStride || (deq && (ldd < n || ldd > kFp4MaxStride)))
+      return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: row stride out of range");
+    if (rows > 0 && (!x || !codes || !scales)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: NULL pointer");
+    if (fmt == KRONQ_NVFP4 && !gscale) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: NVFP4 needs gscale");
+    if (fmt == KRONQ_MXFP4 && gscale) return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: MXFP4 has no tensor scale");
+    if (!aligned(codes, 16) || !aligned(scales, 16))
+      return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: codes and scales must be 16-byte aligned");
+    const int esize = dt == KRONQ_BF16 ? 2 : 4;
+    if (!aligned(x, esize) || (deq && !aligned(deq, esize)) || (gscale && !aligned(gscale, 4)))
+      return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: misaligned pointer");
+    const bool compute = fmt == KRONQ_NVFP4 && !gscale_given;
+    if (compute && rows > 0 &&
+        (!workspace || ws_bytes < kronq_fp4_quantize_workspace_bytes(rows, n, fmt) || !aligned(workspace, 256)))
+      return fail(KRONQ_ERR_INVALID_ARG, "fp4_quantize: workspace too small or not 256-byte aligned");
+    if (rows == 0 && !compute) return KRONQ_OK;
+    cudaStream_t st = as_stream(s);
+    QuantArgs a;
+    a.x = x; a.rows = rows; a.n = n; a.ldx = ldx;
+    a.codes = codes; a.scales = scales;
+    a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
+    a.gscale = gscale;
+    a.partial = nullptr; a.npartial = 0;
+    a.deq = deq; a.ldd = ldd;
+    a.vec_in = aligned(x, 32) && (ldx * esize) % 32 == 0;
+    a.vec_out = deq && aligned(deq, 32) && (ldd * esize) % 32 == 0;
+    a.x_lo = reinterpret_cast<uintptr_t>(x);
+    a.x_hi = a.x_lo + (size_t)(rows > 0 ? (rows - 1) * ldx + n : 0) * esize;
+    if (compute) {
+      uint32_t* partial = rows > 0 ? static_cast<uint32_t*>(workspace) : reinterpret_cast<uint32_t*>(gscale);
+      a.partial = partial;
+      if (rows > 0) {
+        const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), dt == KRONQ_BF16 ? 2 * AMAX_RUNS : AMAX_RUNS), 4);
+        if (dt == KRONQ_BF16) fp4_amax_kernel<true><<<grid, QT, 0, st>>>(a, partial);
+        else fp4_amax_kernel<false><<<grid, QT, 0, st>>>(a, partial);
+        KQ_LAUNCH_CHECK("fp4_amax_kernel");
+        a.npartial = (int)grid;
+      }
     }
-  }
-  const int64_t units = rows * a.lds * (fmt == KRONQ_MXFP4 ? 2 : 1);
-  const unsigned grid = quant_grid(units, 4);
-  a.table = units >= 2 * (int64_t)grid * QT;
-  if (fmt == KRONQ_MXFP4) {
-    if (dt == KRONQ_BF16) fp4_quantize_kernel<KRONQ_MXFP4, true><<<grid, QT, 0, st>>>(a);
-    else fp4_quantize_kernel<KRONQ_MXFP4, false><<<grid, QT, 0, st>>>(a);
-  } else {
-    if (dt == KRONQ_BF16) fp4_quantize_kernel<KRONQ_NVFP4, true><<<grid, QT, 0, st>>>(a);
-    else fp4_quantize_kernel<KRONQ_NVFP4, false><<<grid, QT, 0, st>>>(a);
-  }
-  KQ_LAUNCH_CHECK("fp4_quantize_kernel");
-  return KRONQ_OK;
+    const int64_t units = rows * a.lds * (fmt == KRONQ_MXFP4 ? 2 : 1);
+    const unsigned grid = quant_grid(units, 4);
+    a.table = units >= 2 * (int64_t)grid * QT;
+    if (fmt == KRONQ_MXFP4) {
+      if (dt == KRONQ_BF16) fp4_quantize_kernel<KRONQ_MXFP4, true><<<grid, QT, 0, st>>>(a);
+      else fp4_quantize_kernel<KRONQ_MXFP4, false><<<grid, QT, 0, st>>>(a);
+    } else {
+      if (dt == KRONQ_BF16) fp4_quantize_kernel<KRONQ_NVFP4, true><<<grid, QT, 0, st>>>(a);
+      else fp4_quantize_kernel<KRONQ_NVFP4, false><<<grid, QT, 0, st>>>(a);
+    }
+    KQ_LAUNCH_CHECK("fp4_quantize_kernel");
+    return KRONQ_OK;
+  });
 }
 
 kronq_status kronq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, const float* gscale,
                                   kronq_fp4_format fmt, int64_t rows, int64_t n, void* out, kronq_dtype dt,
                                   int64_t ldo, kronq_stream_t s) {
-  if (!fp4_fmt_ok(fmt)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: bad format");
-  if (dt != KRONQ_BF16 && dt != KRONQ_F32) return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: bad dtype");
-  if (rows < 0 || rows > kFp4MaxDim || n <= 0 || n > kFp4MaxDim)
-    return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: sizes out of range");
-  if (ldo < n) return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: row stride below n");
-  if (rows > 0 && (!codes || !scales || !out)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: NULL pointer");
-  if ((fmt == KRONQ_NVFP4) != (gscale != nullptr))
-    return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: gscale goes with NVFP4 and with it only");
-  const int esize = dt == KRONQ_BF16 ? 2 : 4;
-  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, esize) || (gscale && !aligned(gscale, 4)))
-    return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: misaligned pointer");
-  if (rows == 0) return KRONQ_OK;
-  DequantArgs a;
-  a.codes = codes; a.scales = scales; a.rows = rows; a.n = n;
-  a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
-  a.gscale = gscale; a.out = out; a.ldo = ldo;
-  const int vec_out = aligned(out, 32) && (ldo * esize) % 32 == 0;   // rows are 32-byte aligned
-  const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), UNROLL), 3);
-  cudaStream_t st = as_stream(s);
-  using K = void (*)(const DequantArgs);
-  static const K kernels[8] = {
-      fp4_dequantize_kernel<KRONQ_MXFP4, false, false>, fp4_dequantize_kernel<KRONQ_MXFP4, false, true>,
-      fp4_dequantize_kernel<KRONQ_MXFP4, true, false>,  fp4_dequantize_kernel<KRONQ_MXFP4, true, true>,
-      fp4_dequantize_kernel<KRONQ_NVFP4, false, false>, fp4_dequantize_kernel<KRONQ_NVFP4, false, true>,
-      fp4_dequantize_kernel<KRONQ_NVFP4, true, false>,  fp4_dequantize_kernel<KRONQ_NVFP4, true, true>};
-  kernels[4 * (fmt == KRONQ_NVFP4) + 2 * (dt == KRONQ_BF16) + vec_out]<<<grid, QT, 0, st>>>(a);
-  KQ_LAUNCH_CHECK("fp4_dequantize_kernel");
-  return KRONQ_OK;
+  return fp4_entry([&]() -> kronq_status {
+    if (!fp4_fmt_ok(fmt)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: bad format");
+    if (dt != KRONQ_BF16 && dt != KRONQ_F32) return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: bad dtype");
+    if (rows < 0 || rows > kFp4MaxDim || n <= 0 || n > kFp4MaxDim)
+      return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: sizes out of range");
+    if (ldo < n || ldo > kFp4MaxStride) return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: row stride out of range");
+    if (rows > 0 && (!codes || !scales || !out)) return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: NULL pointer");
+    if ((fmt == KRONQ_NVFP4) != (gscale != nullptr))
+      return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: gscale goes with NVFP4 and with it only");
+    const int esize = dt == KRONQ_BF16 ? 2 : 4;
+    if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, esize) || (gscale && !aligned(gscale, 4)))
+      return fail(KRONQ_ERR_INVALID_ARG, "fp4_dequantize: misaligned pointer");
+    if (rows == 0) return KRONQ_OK;
+    DequantArgs a;
+    a.codes = codes; a.scales = scales; a.rows = rows; a.n = n;
+    a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
+    a.gscale = gscale; a.out = out; a.ldo = ldo;
+    const int vec_out = aligned(out, 32) && (ldo * esize) % 32 == 0;   // rows are 32-byte aligned
+    const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), UNROLL), 3);
+    cudaStream_t st = as_stream(s);
+    using K = void (*)(const DequantArgs);
+    static const K kernels[8] = {
+        fp4_dequantize_kernel<KRONQ_MXFP4, false, false>, fp4_dequantize_kernel<KRONQ_MXFP4, false, true>,
+        fp4_dequantize_kernel<KRONQ_MXFP4, true, false>,  fp4_dequantize_kernel<KRONQ_MXFP4, true, true>,
+        fp4_dequantize_kernel<KRONQ_NVFP4, false, false>, fp4_dequantize_kernel<KRONQ_NVFP4, false, true>,
+        fp4_dequantize_kernel<KRONQ_NVFP4, true, false>,  fp4_dequantize_kernel<KRONQ_NVFP4, true, true>};
+    kernels[4 * (fmt == KRONQ_NVFP4) + 2 * (dt == KRONQ_BF16) + vec_out]<<<grid, QT, 0, st>>>(a);
+    KQ_LAUNCH_CHECK("fp4_dequantize_kernel");
+    return KRONQ_OK;
+  });
 }
 
 }  // extern "C"

@@ -475,6 +475,147 @@ def test_repeats_are_bitwise_equal():
     assert all(torch.equal(y, ys[0]) for y in ys) and all(torch.equal(v, vs[0]) for v in vs)
 
 
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,m,n", [(40, 300, 20000), (257, 200, 9000), (1, 256, 40000), (64, 1030, 8224)])
+def test_matmul_with_split_columns(fmt, dt, T, m, n):
+    assert kq.kronq_fp4_matmul_workspace_bytes(T, m, n, fmt) > 0
+    rng = np.random.default_rng(T + n)
+    x, w = stored(rng.standard_normal((T, n)), fmt), stored(0.02 * rng.standard_normal((m, n)), fmt)
+    big = torch.full((T, m + 3), 9.0, dtype=dt, device=DEV)
+    matmul(x, w, fmt, n, big[:, 1:-2])
+    check(big[:, 1:-2], *fp4.product(x[3], w[3], g_of(x), g_of(w)), n)
+    assert (big[:, 0] == 9.0).all() and (big[:, -2:] == 9.0).all()
+
+
+@pytest.mark.parametrize("T", [1, 4, 11, 16])
+@pytest.mark.parametrize("xdt", [torch.bfloat16, torch.float32])
+def test_matvec_ranges_within_a_token(T, xdt):
+    # spans of 128 columns whose values differ by more than fp16 parts cover,
+    # next to plain ones; E8M0 scales beyond the fp16 range
+    rng = np.random.default_rng(17 + T)
+    n, m = 1300, 200
+    x = rng.standard_normal((T, n)).astype(np.float32)
+    x[0, 130:140] *= 1e-12
+    x[T - 1, 300] = 1e20
+    x[T // 2, 600:728] = 0.0
+    x[0, 1290] = 1e-40
+    w = 0.02 * rng.standard_normal((m, n))
+    w[3, 256:288] *= 1e-15
+    w[5, 640:672] *= 1e12
+    xt = torch.from_numpy(x).to(xdt)
+    for fmt in (MX, NV):
+        q = stored(w, fmt)
+        y = torch.empty(T, m, device=DEV)
+        kq.kronq_fp4_matvec(xt.to(DEV), q[0], q[1], fmt, y, wg=q[2])
+        y64, S = fp4.product(xt.double().numpy(), q[3], None, g_of(q))
+        # 2^-149: products below the smallest float32
+        assert (np.abs(y.double().cpu().numpy() - y64) <= tolerance(n, S, y64, torch.float32) + n * 2.0 ** -149).all()
+
+
+def test_matvec_loud_column_with_zero_weights():
+    # a column 2^40 times the others whose weights are all zero: the others count in full
+    n, m = 256, 64
+    w = torch.randn(m, n, dtype=torch.float64, generator=torch.Generator().manual_seed(3)).numpy()
+    w[:, 17] = 0.0
+    x = np.ones((2, n), np.float32)
+    x[:, 17] = 2.0 ** 40
+    for fmt in (MX, NV):
+        for xdt in (torch.bfloat16, torch.float32):
+            q = stored(w, fmt)
+            y = torch.empty(2, m, device=DEV)
+            kq.kronq_fp4_matvec(torch.from_numpy(x).to(xdt).to(DEV), q[0], q[1], fmt, y, wg=q[2])
+            check(y, *fp4.product(x, q[3], None, g_of(q)), n)
+
+
+def test_offsets_beyond_32_bits():
+    """Arrays of more than 2^32 bytes and elements: each call's last rows equal
+    those of the same call on these rows alone."""
+    rows, n = 70000, 65536
+    x = torch.empty(rows, n, dtype=torch.bfloat16, device=DEV).normal_()
+    c = torch.empty(rows, kq.kronq_fp4_code_row_bytes(n), dtype=torch.uint8, device=DEV)
+    s = torch.empty(rows, kq.kronq_fp4_scale_row_bytes(NV, n), dtype=torch.uint8, device=DEV)
+    g = torch.full((1,), 0.002, device=DEV)
+    kq.kronq_fp4_quantize(x, NV, c, s, gscale=g, gscale_given=True, deq=x)
+    tail = x[-5:].clone()
+    x.zero_()
+    kq.kronq_fp4_dequantize(c, s, NV, x, gscale=g)
+    assert torch.equal(x[-5:], tail) and bool(torch.isfinite(tail).all()) and float(tail.float().std()) > 0.5
+    del x
+    # the last rows' product with two tokens, alone and among all rows
+    xf = torch.randn(2, n, device=DEV)
+    y, z = torch.empty(2, rows, device=DEV), torch.empty(2, 64, device=DEV)
+    kq.kronq_fp4_matvec(xf, c, s, NV, y, wg=g)
+    kq.kronq_fp4_matvec(xf, c[-64:], s[-64:], NV, z, wg=g)
+    # the columns may be split otherwise: (n / 16 + 4) 2^-22 of sum |x w|, whose mean is n 0.8 0.8
+    assert float((y[:, -64:] - z).abs().max()) < (n / 16 + 4) * 2.0 ** -22 * n
+    # two experts, the second's rows beyond 2^31 bytes of codes
+    xc, xs = c[:3].clone(), s[:3].clone()
+    off = torch.tensor([0, 1, 3], dtype=torch.int32, device=DEV)
+    gg = torch.ones(2, device=DEV)
+    out = torch.empty(3, rows // 2, device=DEV)
+    kq.kronq_fp4_grouped_matmul(xc, xs, off, c.view(2, rows // 2, -1), s.view(2, rows // 2, -1), NV, n, out, xg=g, wg=gg)
+    want = torch.empty(3, 64, device=DEV)
+    kq.kronq_fp4_matmul(xc, xs, c[-64:], s[-64:], NV, n, want, xg=g, wg=gg[:1])
+    assert float((out[1:, -64:] - want[1:]).abs().max()) < (n / 16 + 4) * 2.0 ** -22 * n * 500 * 0.002
+    del out, c, s
+    # an output of more than 2^31 elements
+    T, m, n = 66000, 34000, 64
+    wc = torch.randint(0, 256, (m, 32), dtype=torch.uint8, device=DEV)
+    xc = torch.randint(0, 256, (T, 32), dtype=torch.uint8, device=DEV)
+    one = torch.full((m, 16), 127, dtype=torch.uint8, device=DEV)
+    ones = torch.full((T, 16), 127, dtype=torch.uint8, device=DEV)
+    y = torch.empty(T, m, dtype=torch.bfloat16, device=DEV)
+    kq.kronq_fp4_matmul(xc, ones, wc, one, MX, n, y)
+    z = torch.empty(9, m, dtype=torch.bfloat16, device=DEV)
+    kq.kronq_fp4_matmul(xc[-9:], ones[-9:], wc, one, MX, n, z)
+    assert torch.equal(y[-9:], z)
+
+
+def test_first_call_inside_a_capture():
+    """In a process of its own, the first 4-bit calls of all are captured ones."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import post_quantization_kronq_b200 as kq
+d = "cuda"
+x = torch.randn(24, 512, device=d); w = torch.randn(96, 512, device=d)
+q = lambda r, b: torch.zeros(r, b, dtype=torch.uint8, device=d)
+xc, xs, wc, ws = q(24, 256), q(24, 16), q(96, 256), q(96, 16)
+y, v, dx, dw = torch.zeros(24, 96, device=d), torch.zeros(3, 96, device=d), torch.empty_like(x), torch.empty_like(w)
+off = torch.tensor([0, 24], dtype=torch.int32, device=d)
+z = torch.zeros(24, 96, device=d)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    kq.kronq_fp4_quantize(x, kq.MXFP4, xc, xs, deq=dx)
+    kq.kronq_fp4_quantize(w, kq.MXFP4, wc, ws, deq=dw)
+    kq.kronq_fp4_matmul(xc, xs, wc, ws, kq.MXFP4, 512, y)
+    kq.kronq_fp4_grouped_matmul(xc, xs, off, wc[None], ws[None], kq.MXFP4, 512, z)
+    kq.kronq_fp4_matvec(x[:3], wc, ws, kq.MXFP4, v)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, z)
+assert (y - dx @ dw.T).abs().max() < 1e-2 and (v - x[:3] @ dw.T).abs().max() < 1e-2
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=__file__.rsplit("/", 2)[0])
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_expanded_rows_are_refused():
+    c = torch.zeros(4, 32, dtype=torch.uint8, device=DEV)
+    s = torch.zeros(4, 16, dtype=torch.uint8, device=DEV)
+    x = torch.zeros(1, 64, device=DEV).expand(4, 64)
+    for call in (lambda: kq.kronq_fp4_quantize(x, MX, c, s), lambda: kq.kronq_fp4_dequantize(c, s, MX, x),
+                 lambda: kq.kronq_fp4_matvec(x, c, s, MX, torch.zeros(4, 4, device=DEV)),
+                 lambda: kq.kronq_fp4_matmul(c, s, c, s, MX, 64, torch.zeros(1, 4, device=DEV).expand(4, 4))):
+        with pytest.raises(kq.KronqError):
+            call()
+
+
 def test_python_refusals_on_the_device():
     c = torch.zeros(4, 32, dtype=torch.uint8, device=DEV)
     s = torch.zeros(4, 16, dtype=torch.uint8, device=DEV)
