@@ -404,7 +404,7 @@ def _fp4_ws(ws, need, args, device):
         ws = workspace(nbytes, device)
     elif ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous on {device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+    return ws.data_ptr(), ws.nbytes, ws
 
 
 def _fp4_dtype(t):

@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace kq {
@@ -28,6 +30,14 @@ inline int64_t fp4_scale_row(int fmt, int64_t n) { return ceil_div(ceil_div(n, f
 // within 64 bits).
 constexpr int64_t kFp4MaxDim = int64_t(1) << 30;
 constexpr int64_t kFp4MaxStride = int64_t(1) << 32;
+
+// Number of SMs of the current device, and a kernel's dynamic shared memory
+// limit raised on it, each asked of the runtime once per device (a decoded
+// token's calls are shorter than the questions).  `done` is the kernel's own
+// array of kMaxDevices flags.
+constexpr int kMaxDevices = 64;
+int fp4_sms(int* dev);
+cudaError_t fp4_allow_smem(const void* fn, int bytes, int dev, std::atomic<bool>* done);
 
 // Runs a C entry point's body; no exception (out of host memory, in building
 // an error message) passes the C boundary.

@@ -37,6 +37,28 @@ kronq_status check_tokens(const char* name, int fmt, int64_t T, const void* xc, 
 }
 
 }  // namespace
+
+int fp4_sms(int* dev) {
+  static std::atomic<int> known[kMaxDevices];
+  int d = 0, v = 148;
+  if (cudaGetDevice(&d) != cudaSuccess) d = -1;
+  if (dev) *dev = d;
+  if (d < 0 || d >= kMaxDevices) return sm_count();
+  v = known[d].load(std::memory_order_relaxed);
+  if (v == 0) {
+    v = sm_count();
+    known[d].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
+cudaError_t fp4_allow_smem(const void* fn, int bytes, int dev, std::atomic<bool>* done) {
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = allow_smem(fn, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 }  // namespace kq
 
 using namespace kq;

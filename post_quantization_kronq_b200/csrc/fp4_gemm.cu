@@ -33,8 +33,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <atomic>
-
 #include "fp4.cuh"
 #include "fp4_products.h"
 #include "internal.h"
@@ -591,9 +589,9 @@ using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
 // Most pairs of the kernel that run at once on the current device (a property
 // of the device, asked for once per kernel), 0 on error.
 int active_pairs(Kernel fn, int which, int smem) {
-  static std::atomic<int> known[64][8];
+  static std::atomic<int> known[kMaxDevices][6];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   int v = known[dev][which].load(std::memory_order_relaxed);
   if (v > 0) return v;
   if (allow_smem(reinterpret_cast<const void*>(fn), smem) != cudaSuccess) return 0;
@@ -643,8 +641,9 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!tma_map_2d(&mw, u8, 1, g.wc, bytes, (g.offsets ? g.E : 1) * g.m, ldc, 128, GH) ||
       !tma_map_2d(&mx, u8, 1, g.xc, bytes, g.T, ldc, 128, XROWS) ||
-      !tma_map_2d(&mxf, u8, 1, g.xc, bytes, g.T, ldc, 128, GH))
+      (g.T > GN - NG && !tma_map_2d(&mxf, u8, 1, g.xc, bytes, g.T, ldc, 128, GH)))
     return fail(KRONQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (fp4 product)");
+  if (g.T <= GN - NG) mxf = mx;   // no tile of GN tokens
   GemmArgs a;
   a.xs = g.xs; a.ws = g.ws; a.xg = g.xg; a.wg = g.wg;
   a.offsets = g.offsets;

@@ -499,10 +499,11 @@ int64_t slice_columns(int64_t T, int64_t m, int64_t n, bool x_f32) {
 }
 
 template <int FMT, bool XF32>
-kronq_status launch_vec(const VecArgs& a, dim3 grid, int smem, cudaStream_t st) {
+kronq_status launch_vec(const VecArgs& a, dim3 grid, int smem, int dev, cudaStream_t st) {
+  static std::atomic<bool> done[2][kMaxDevices];
   void (*fn)(const VecArgs) = a.T > 8 ? fp4_matvec_kernel<FMT, XF32, 2> : fp4_matvec_kernel<FMT, XF32, 1>;
   // one limit for every call, so that calls of other threads do not lower it
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), RBYTES + XSMEM + 4 * 1024);
+  cudaError_t e = fp4_allow_smem(reinterpret_cast<const void*>(fn), RBYTES + XSMEM + 4 * 1024, dev, done[a.T > 8]);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(fp4 matvec)");
   fn<<<grid, VT, smem, st>>>(a);
   KQ_LAUNCH_CHECK("fp4_matvec_kernel");
@@ -537,14 +538,15 @@ kronq_status fp4_matvec(const Fp4Matvec& v, int fmt, cudaStream_t st) {
   while (a.wk > 1 && (a.wk > pairs || (pairs < 4 * a.wk && tiles * (a.wk / 2) / VW * slices >= 2 * CTAS * 148)))
     a.wk /= 2;
   const int64_t groups = ceil_div(tiles, VW / a.wk);   // row tiles that a CTA takes at once
-  int64_t gx = CTAS * (int64_t)sm_count() / slices;
+  int dev = 0;
+  int64_t gx = CTAS * (int64_t)fp4_sms(&dev) / slices;
   if (gx < 1) gx = 1;
   if (gx > groups) gx = groups;
   const dim3 grid((unsigned)gx, (unsigned)slices);
   const int smem = RBYTES + (int)(v.T * (v.x_f32 ? 2 : 1)) * a.xrow + (int)(kslice / SPAN) * span_bytes(v.T);
   kronq_status r;
-  if (fmt == KRONQ_MXFP4) r = v.x_f32 ? launch_vec<KRONQ_MXFP4, true>(a, grid, smem, st) : launch_vec<KRONQ_MXFP4, false>(a, grid, smem, st);
-  else r = v.x_f32 ? launch_vec<KRONQ_NVFP4, true>(a, grid, smem, st) : launch_vec<KRONQ_NVFP4, false>(a, grid, smem, st);
+  if (fmt == KRONQ_MXFP4) r = v.x_f32 ? launch_vec<KRONQ_MXFP4, true>(a, grid, smem, dev, st) : launch_vec<KRONQ_MXFP4, false>(a, grid, smem, dev, st);
+  else r = v.x_f32 ? launch_vec<KRONQ_NVFP4, true>(a, grid, smem, dev, st) : launch_vec<KRONQ_NVFP4, false>(a, grid, smem, dev, st);
   if (r != KRONQ_OK || slices == 1) return r;
   fp4_matvec_join_kernel<<<(unsigned)ceil_div(v.T * v.m, 256), 256, 0, st>>>(a, (int)slices);
   KQ_LAUNCH_CHECK("fp4_matvec_join_kernel");

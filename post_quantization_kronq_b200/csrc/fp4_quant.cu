@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(QT, 3) fp4_dequantize_kernel(const DequantArgs
 // Blocks for `total` units of one thread each: at most as many as run at once
 // (per_sm: the kernel's registers allow that many).
 unsigned quant_grid(int64_t total, int per_sm) {
-  const int64_t want = ceil_div(total, QT), cap = std::min<int64_t>(per_sm * (int64_t)sm_count(), MAX_PARTIALS);
+  const int64_t want = ceil_div(total, QT), cap = std::min<int64_t>(per_sm * (int64_t)fp4_sms(nullptr), MAX_PARTIALS);
   return (unsigned)(want < 1 ? 1 : want < cap ? want : cap);
 }
 
