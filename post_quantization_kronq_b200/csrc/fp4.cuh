@@ -65,6 +65,20 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t b) {
   return FMT == KRONQ_MXFP4 ? e8m0_value(b) : e4m3_value(b);
 }
 
+// Sum of `count` partial sums `stride` apart, in order, eight loads at a time.
+__device__ __forceinline__ float fp4_join(const float* part, int64_t stride, int count) {
+  float v = 0.f;
+  for (int s = 0; s < count; s += 8) {
+    float p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = s + k < count ? part[(s + k) * stride] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (s + k < count) v += p[k];
+  }
+  return v;
+}
+
 // Two E2M1 codes (a byte, the first in the low half) as a pair of halves.
 __device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t byte) {
   uint32_t h;

@@ -491,7 +491,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!__shfl_sync(0xffffffffu, good, 0)) break;
       tc_fence_after();
       const int64_t r = t.m0 + GH * (int64_t)rank + q * 32 + lane;
-      const float xg = !PART && a.xg ? *a.xg : 1.f, wg = !PART && a.wg ? a.wg[t.e] : 1.f;
+      // both tensor scales as one factor, unless their product leaves float32's normal range
+      float xg = !PART && a.xg ? *a.xg : 1.f, wg = !PART && a.wg ? a.wg[t.e] : 1.f;
+      const float both = __fmul_rn(xg, wg);
+      const bool one = PART || (both >= 1.17549435e-38f && both <= 3.40282347e38f);
+      if (one) xg = both;
       const int groups = t.cols / 64;    // 32-column groups of this warp: half, half + 2, ...
       const int64_t ld = PART ? a.m : a.ldy;
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -505,8 +509,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[2 * e]), xg), wg),
-                                                             __fmul_rn(__fmul_rn(__uint_as_float(v[2 * e + 1]), xg), wg));
+              float lo = __fmul_rn(__uint_as_float(v[2 * e]), xg), hi = __fmul_rn(__uint_as_float(v[2 * e + 1]), xg);
+              if (!one) lo = __fmul_rn(lo, wg), hi = __fmul_rn(hi, wg);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
               pk[g][e] = *reinterpret_cast<const uint32_t*>(&h);
             }
           }
@@ -536,7 +541,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int64_t tk = t.t0 + (2 * g + half) * 32;
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (r < a.m && tk + e < t.t1) y[(tk + e) * ld + r] = __fmul_rn(__fmul_rn(__uint_as_float(v[e]), xg), wg);
+            if (r < a.m && tk + e < t.t1) {
+              const float f = PART ? __uint_as_float(v[e]) : __fmul_rn(__uint_as_float(v[e]), xg);
+              y[(tk + e) * ld + r] = one ? f : __fmul_rn(f, wg);
+            }
           __syncwarp();
         }
         tc_fence_before();
@@ -562,9 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 __global__ void __launch_bounds__(256) fp4_join_kernel(const GemmArgs a, int bf16) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = a.T * a.m;
   if (i >= total) return;
-  float v = 0.f;
-  for (int s = 0; s < a.splits; ++s) v += a.part[s * total + i];
-  v = __fmul_rn(__fmul_rn(v, a.xg ? *a.xg : 1.f), a.wg ? *a.wg : 1.f);
+  const float v = __fmul_rn(__fmul_rn(fp4_join(a.part + i, total, a.splits), a.xg ? *a.xg : 1.f), a.wg ? *a.wg : 1.f);
   const int64_t t = i / a.m, r = i - t * a.m;
   if (bf16) static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + r] = __float2bfloat16_rn(v);
   else static_cast<float*>(a.y)[t * a.ldy + r] = v;

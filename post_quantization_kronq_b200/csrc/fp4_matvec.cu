@@ -476,9 +476,7 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
 __global__ void __launch_bounds__(256) fp4_matvec_join_kernel(const VecArgs a, int slices) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = (int64_t)a.T * a.m;
   if (i >= total) return;
-  float v = 0.f;
-  for (int s = 0; s < slices; ++s) v += a.part[s * total + i];
-  v = __fmul_rn(v, a.wg ? *a.wg : 1.f);
+  const float v = __fmul_rn(fp4_join(a.part + i, total, slices), a.wg ? *a.wg : 1.f);
   const int64_t tk = i / a.m, r = i - tk * a.m;
   if (a.y_bf16) static_cast<__nv_bfloat16*>(a.y)[tk * a.ldy + r] = __float2bfloat16_rn(v);
   else static_cast<float*>(a.y)[tk * a.ldy + r] = v;
