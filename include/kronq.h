@@ -24,6 +24,9 @@
  *     dequant + BiIP matvec for single-token decode) -> kronq_decode_matvec
  *   - two-sided rounding that uses H_G inside the sweep ("BaKron" abstract:
  *     GPTQ on vec(W) under H_X (x) H_G)            -> kronq_quantize_two_sided
+ *   - microscaled 4-bit floating point (MXFP4, NVFP4): quantiser, its
+ *     inverse, products of quantised matrices (plain and grouped by expert)
+ *     and of a few full-precision tokens            -> kronq_fp4_*
  *
  * Conventions (all calls):
  *   - Matrices are row-major.  W is m x n (out x in), X is T x n, G is T x m.
@@ -498,7 +501,9 @@ kronq_status kronq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, c
  * both quantised in the same format: y (T x m, dtype ydt, row stride ldy),
  * products exact, sums in float32, the tensor scales applied to the sums.
  * workspace: kronq_fp4_matmul_workspace_bytes(T, m, n, fmt) bytes (0 where n
- * is not split), 256-byte aligned.  T may be 0.  y may not overlap an input.
+ * is not split), 256-byte aligned; calls that may overlap on the GPU, replayed
+ * graphs among them, each need their own.  T may be 0, n at most 2^24 and the
+ * row strides of all 4-bit calls at most 2^32.  y may not overlap an input.
  * Asynchronous on s. */
 size_t kronq_fp4_matmul_workspace_bytes(int64_t T, int64_t m, int64_t n, kronq_fp4_format fmt);
 kronq_status kronq_fp4_matmul(const uint8_t* xc, const uint8_t* xs, const float* xg, const uint8_t* wc,
@@ -508,7 +513,9 @@ kronq_status kronq_fp4_matmul(const uint8_t* xc, const uint8_t* xs, const float*
 
 /* kronq_fp4_matvec -- y = X W^T for at most KRONQ_FP4_MATVEC_MAX_TOKENS
  * tokens X (T x n, bf16 or float32, row stride ldx) that are not quantised
- * (single-token decode with 4-bit weights); products and sums in float32.
+ * (single-token decode with 4-bit weights).  Weights and bf16 tokens enter the
+ * products exactly, float32 tokens to 2^-22 of each value or better; sums in
+ * float32, in an order that depends on the sizes alone.  n at most 2^24.
  * Other arguments as kronq_fp4_matmul. */
 size_t kronq_fp4_matvec_workspace_bytes(int64_t T, int64_t m, int64_t n, kronq_fp4_format fmt);
 kronq_status kronq_fp4_matvec(const void* x, kronq_dtype xdt, int64_t ldx, const uint8_t* wc, const uint8_t* ws,

@@ -315,7 +315,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       // loop runs over whole loader groups without a branch for each chunk,
       // counters advance by increments and descriptors by adding to their low
       // words.  A group's scales go to TMEM while the group before is
-      // multiplied, chunk by chunk, into the other of two buffers.
+      // multiplied, chunk by chunk, into the other of two buffers (copies and
+      // MMAs of one thread run in the order of their issue, so a copy does not
+      // overtake the MMAs that still read its buffer).
       constexpr int CH = 2 * CPP;             // chunks of a group
       constexpr uint32_t kCols = 48 / CPP;    // TMEM columns of a chunk's scales
       uint32_t s = 0, ph = 0;                 // stage of codes

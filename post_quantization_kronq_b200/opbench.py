@@ -8,6 +8,11 @@
     python -m post_quantization_kronq_b200.opbench kronfactors --est flipflop --tokens 131072 --m 4096 --n 4096
     python -m post_quantization_kronq_b200.opbench decode --m 4096 --n 4096 --bits 2 --reps 100
     python -m post_quantization_kronq_b200.opbench twosided --m 4096 --n 4096 --bits 2 [--u-given]
+    python -m post_quantization_kronq_b200.opbench fp4_quantize --fmt nvfp4 --m 8192 --n 8192
+    python -m post_quantization_kronq_b200.opbench fp4_dequantize --fmt mxfp4 --m 8192 --n 8192
+    python -m post_quantization_kronq_b200.opbench fp4_matmul --fmt nvfp4 --tokens 4096 --m 8192 --n 8192
+    python -m post_quantization_kronq_b200.opbench fp4_matvec --fmt nvfp4 --tokens 1 --m 28672 --n 8192
+    python -m post_quantization_kronq_b200.opbench fp4_grouped --experts 8 --tokens 4096 --m 14336 --n 4096
 
 Meant for profiling a single kernel family (e.g. under ncu) at a size that
 is smaller than the full benchmark; prints one JSON line with the mean
@@ -25,6 +30,53 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 
+def fp4_op(a, dev):
+    """(call, units) of one of the 4-bit floating-point operators; bf16 tokens and outputs."""
+    import torch
+
+    import post_quantization_kronq_b200 as kq
+
+    fmt = kq.NVFP4 if a.fmt == "nvfp4" else kq.MXFP4
+
+    def arrays(rows):
+        return (torch.empty(rows, kq.kronq_fp4_code_row_bytes(a.n), dtype=torch.uint8, device=dev),
+                torch.empty(rows, kq.kronq_fp4_scale_row_bytes(fmt, a.n), dtype=torch.uint8, device=dev),
+                torch.empty(1, device=dev) if fmt == kq.NVFP4 else None)
+
+    def quantized(x):
+        c, s, g = arrays(x.shape[0])
+        kq.kronq_fp4_quantize(x, fmt, c, s, gscale=g)
+        return c, s, g
+
+    per = 0.5 + 1 / (16 if fmt == kq.NVFP4 else 32)
+    rows = a.m * (a.experts if a.op == "fp4_grouped" else 1)
+    W = 0.02 * torch.randn(rows, a.n, device=dev).to(torch.bfloat16)
+    if a.op == "fp4_quantize":
+        c, s, g = arrays(a.m)
+        ws = kq.workspace(kq.kronq_fp4_quantize_workspace_bytes(a.m, a.n, fmt), dev)
+        return (lambda: kq.kronq_fp4_quantize(W, fmt, c, s, gscale=g, ws=ws)), {"bytes": a.m * a.n * (2 + per)}
+    w = quantized(W)
+    if a.op == "fp4_dequantize":
+        return (lambda: kq.kronq_fp4_dequantize(w[0], w[1], fmt, W, gscale=w[2])), {"bytes": a.m * a.n * (2 + per)}
+    X = torch.randn(a.tokens, a.n, device=dev).to(torch.bfloat16)
+    y = torch.empty(a.tokens, a.m, dtype=torch.bfloat16, device=dev)
+    units = {"bytes": rows * a.n * per + a.tokens * (a.n * per + 2 * a.m), "flops": 2 * a.tokens * a.m * a.n}
+    if a.op == "fp4_matvec":
+        ws = kq.workspace(kq.kronq_fp4_matvec_workspace_bytes(a.tokens, a.m, a.n, fmt), dev)
+        return (lambda: kq.kronq_fp4_matvec(X, w[0], w[1], fmt, y, wg=w[2], ws=ws)), units
+    x = quantized(X)
+    if a.op == "fp4_matmul":
+        ws = kq.workspace(kq.kronq_fp4_matmul_workspace_bytes(a.tokens, a.m, a.n, fmt), dev)
+        return (lambda: kq.kronq_fp4_matmul(x[0], x[1], w[0], w[1], fmt, a.n, y, xg=x[2], wg=w[2], ws=ws)), units
+    off = torch.tensor([e * a.tokens // a.experts for e in range(a.experts + 1)], dtype=torch.int32, device=dev)
+    wc, wsc = w[0].view(a.experts, a.m, -1), w[1].view(a.experts, a.m, -1)
+    wg = None if w[2] is None else w[2].expand(a.experts).contiguous()
+    return (lambda: kq.kronq_fp4_grouped_matmul(x[0], x[1], off, wc, wsc, fmt, a.n, y, xg=x[2], wg=wg)), units
+
+
+FP4_OPS = ["fp4_quantize", "fp4_dequantize", "fp4_matmul", "fp4_matvec", "fp4_grouped"]
+
+
 def main(argv=None):
     import torch
 
@@ -34,7 +86,9 @@ def main(argv=None):
 
     ap = argparse.ArgumentParser()
     ap.add_argument("op", choices=["accumulate", "biip", "biip_inverse", "quantize", "pack", "kronfactors",
-                                   "decode", "twosided"])
+                                   "decode", "twosided"] + FP4_OPS)
+    ap.add_argument("--fmt", choices=["mxfp4", "nvfp4"], default="nvfp4")
+    ap.add_argument("--experts", type=int, default=8)
     ap.add_argument("--u-given", action="store_true",
                     help="twosided: factor once, time the sweep alone (KRONQ_U_GIVEN)")
     ap.add_argument("--est", choices=["input", "marginal", "frobenius", "flipflop"], default="flipflop")
@@ -49,7 +103,9 @@ def main(argv=None):
     a = ap.parse_args(argv)
     dev = torch.device("cuda", 0)
     s = torch.cuda.current_stream()
-    if a.op == "accumulate":
+    if a.op in FP4_OPS:
+        run, units = fp4_op(a, dev)
+    elif a.op == "accumulate":
         X = llama_layer(8, a.d, a.tokens, seed=1, device=dev)[1]
         H = torch.empty(a.d, a.d, device=dev)
         run = lambda: kq.kronq_accumulate_factors(X, H, zero_first=True)  # noqa: E731
@@ -152,8 +208,10 @@ def main(argv=None):
     e1.record(s)
     torch.cuda.synchronize()
     ms = e0.elapsed_time(e1) / a.reps
-    if a.op in ("decode", "biip_inverse"):
+    if a.op in ["decode", "biip_inverse"] + FP4_OPS:
         units["gbs"] = units["bytes"] / (ms / 1e3) / 1e9
+    if a.op in FP4_OPS and "flops" in units:
+        units["tflops"] = units["flops"] / (ms / 1e3) / 1e12
     if a.op == "twosided":
         units["info"] = info.tolist()
         units["tflops"] = units["flops"] / (ms / 1e3) / 1e12
