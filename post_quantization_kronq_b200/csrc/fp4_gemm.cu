@@ -71,6 +71,7 @@ struct GemmArgs {
   int splits, per_split;  // chunks of a split
   void* y;
   int64_t ldy;
+  int y_pairs;            // bf16 rows are 4-byte aligned
   float* part;            // split partial sums [split][T][m], or NULL
 };
 
@@ -522,14 +523,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(lead);
         uint16_t* y = static_cast<uint16_t*>(a.y);
+        const bool rows32 = t.m0 + GH * (int64_t)rank + q * 32 + 32 <= a.m;   // the warp's rows are all there
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           if (g < groups) {
             const int64_t tk = t.t0 + (2 * g + half) * 32;
+            if (a.y_pairs && rows32 && tk + 32 <= t.t1) {
+              // neighbouring lanes exchange halves: an even lane stores two rows
+              // of the first token of a pair, an odd lane those of the second
+              const uint32_t pick = (lane & 1) ? 0x3276u : 0x5410u;
+              uint16_t* o = y + (tk + (lane & 1)) * ld + (r & ~int64_t(1));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              if (r < a.m && tk + 2 * e < t.t1) y[(tk + 2 * e) * ld + r] = (uint16_t)(pk[g][e] & 0xFFFFu);
-              if (r < a.m && tk + 2 * e + 1 < t.t1) y[(tk + 2 * e + 1) * ld + r] = (uint16_t)(pk[g][e] >> 16);
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, pk[g][e], 1);
+                *reinterpret_cast<uint32_t*>(o) = __byte_perm(pk[g][e], other, pick);
+                o += 2 * ld;
+              }
+            } else {
+              uint16_t* o = y + tk * ld + r;
+              const int left = (int)min(t.t1 - tk, (int64_t)32);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                if (r < a.m && 2 * e < left) o[0] = (uint16_t)(pk[g][e] & 0xFFFFu);
+                if (r < a.m && 2 * e + 1 < left) o[ld] = (uint16_t)(pk[g][e] >> 16);
+                o += 2 * ld;
+              }
             }
           }
         }
@@ -541,12 +559,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld_32x32b_x32(acc + (uint32_t)(2 * g + half) * 32, v);
           tmem_wait_ld();
           const int64_t tk = t.t0 + (2 * g + half) * 32;
+          const int left = (int)min(t.t1 - tk, (int64_t)32);
+          float* o = y + tk * ld + r;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (r < a.m && tk + e < t.t1) {
+          for (int e = 0; e < 32; ++e) {
+            if (r < a.m && e < left) {
               const float f = PART ? __uint_as_float(v[e]) : __fmul_rn(__uint_as_float(v[e]), xg);
-              y[(tk + e) * ld + r] = one ? f : __fmul_rn(f, wg);
+              *o = one ? f : __fmul_rn(f, wg);
             }
+            o += ld;
+          }
           __syncwarp();
         }
         tc_fence_before();
@@ -664,6 +686,7 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   a.per_split = g.offsets ? a.nchunks : (int)split_chunks(g.T, g.m, g.n);
   a.splits = (int)ceil_div(a.nchunks, a.per_split);
   a.y = g.y; a.ldy = g.ldy;
+  a.y_pairs = g.y_bf16 && aligned(g.y, 4) && g.ldy % 2 == 0;
   a.part = a.splits > 1 ? static_cast<float*>(g.workspace) : nullptr;
   static const Kernel kernels[6] = {fp4_gemm_kernel<KRONQ_MXFP4, false, false>, fp4_gemm_kernel<KRONQ_MXFP4, true, false>,
                                     fp4_gemm_kernel<KRONQ_MXFP4, false, true>, fp4_gemm_kernel<KRONQ_NVFP4, false, false>,
