@@ -734,7 +734,7 @@ kronq_status kronq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, c
     a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
     a.gscale = gscale; a.out = out; a.ldo = ldo;
     const int vec_out = aligned(out, 32) && (ldo * esize) % 32 == 0;   // rows are 32-byte aligned
-    const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), UNROLL), 3);
+    const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), UNROLL), 6);
     cudaStream_t st = as_stream(s);
     using K = void (*)(const DequantArgs);
     static const K kernels[8] = {
