@@ -12,16 +12,22 @@
 //
 // Scales: the tensor core wants, for 128 rows and 4 scale bytes, 32 lanes x 4
 // words with row r in lane r % 32, word r / 32.  The user's layout is row by
-// row, so loader warps read 16 bytes of four rows 32 apart, transpose
-// the 4 x 4 words in registers and store 16-byte rows of four such 512-byte
-// atoms; tcgen05.cp spreads an atom over TMEM, one loader group ahead of its MMAs.
+// row, so loader warps read 16 bytes of four rows 32 apart, transpose the
+// 4 x 4 words in registers and store 16-byte rows of four such 512-byte atoms;
+// tcgen05.cp spreads an atom over TMEM, one loader group ahead of its MMAs.
 // They work in groups of two such pieces (32 bytes of scales of a row), four
 // groups in flight in registers and two or four in shared memory, because a
 // load, its way to the barrier and the copy take longer than the MMAs of a few
-// chunks.  A tile of 256 x 256
-// leaves 256 of the 512 TMEM columns for scales; the eight epilogue warps
-// drain the accumulator into registers first and release it before they
-// store.
+// chunks.  A tile of 256 x 256 leaves 256 of the 512 TMEM columns for scales;
+// the eight epilogue warps drain the accumulator into registers first and
+// release it before they store.
+//
+// Bound by the 1 kW power cap for long runs of large products (2048 x 28672 x
+// 8192 NVFP4 232 us, 4.2 PFLOP/s at 1.45 GHz; 8192 x 8192 x 28672 MXFP4 735 us, 5.2
+// PFLOP/s at 1.15 GHz, 0.85 and more of the tensor rate at that clock), by the
+// supply of operands and scales at full clocks, by HBM for few tokens (16 tokens,
+// 8192 x 28672 NVFP4 32 us, 0.62 of the measured rate with the columns split),
+// by latency below that (100 x 1000 x 4095 11 us).
 //
 // The odd CTA's loaders arrive at the even CTA's barrier, whose MMA thread
 // copies the scales of both.  The arrival does not release at cluster scope
