@@ -642,7 +642,10 @@ int active_pairs(Kernel fn, int which, int smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)(2 * (sm_count() / 2)));
-  if (cudaOccupancyMaxActiveClusters(&v, reinterpret_cast<const void*>(fn), &cfg) != cudaSuccess || v < 1) return 0;
+  if (cudaOccupancyMaxActiveClusters(&v, reinterpret_cast<const void*>(fn), &cfg) != cudaSuccess || v < 1) {
+    cudaGetLastError();
+    return 0;
+  }
   known[dev][which].store(v, std::memory_order_relaxed);
   return v;
 }
@@ -715,7 +718,10 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernels[which], mw, mx, mxf, a);
   count_launch();
-  if (e != cudaSuccess) return cuda_fail(e, "fp4_gemm_kernel");
+  if (e != cudaSuccess) {
+    cudaGetLastError();   // the next launch's check is not to find this one's error
+    return cuda_fail(e, "fp4_gemm_kernel");
+  }
   if (a.part) {
     fp4_join_kernel<<<(unsigned)ceil_div(g.T * g.m, 256), 256, 0, s>>>(a, g.y_bf16);
     KQ_LAUNCH_CHECK("fp4_join_kernel");

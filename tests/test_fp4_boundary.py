@@ -40,7 +40,7 @@ def quantize(x=P, dt=1, rows=8, n=64, ldx=64, fmt=1, codes=P, scales=P, g=P, giv
     dict(fmt=2), dict(dt=2), dict(rows=-1), dict(n=0), dict(n=BIG, ldx=BIG), dict(ldx=63), dict(deq=P, ldd=63),
     dict(x=None), dict(codes=None), dict(scales=None), dict(g=None), dict(fmt=0), dict(codes=ctypes.c_void_p(4104)),
     dict(scales=ctypes.c_void_p(4104)), dict(x=ODD), dict(deq=ODD, ldd=64), dict(g=ODD),
-    dict(given=0), dict(given=0, ws=P, nb=16), dict(given=0, ws=ctypes.c_void_p(4104), nb=1 << 20)])
+    dict(ldx=(1 << 32) + 1), dict(deq=P, ldd=(1 << 32) + 1), dict(given=0), dict(given=0, ws=P, nb=16), dict(given=0, ws=ctypes.c_void_p(4104), nb=1 << 20)])
 def test_quantize_refusals(kw):
     assert quantize(**kw) == BAD
     assert b"fp4_quantize" in L.kronq_last_error()
@@ -55,7 +55,7 @@ def dequantize(codes=P, scales=P, g=P, fmt=1, rows=8, n=64, out=P, dt=1, ldo=64)
 
 
 @pytest.mark.parametrize("kw", [
-    dict(fmt=-1), dict(dt=5), dict(rows=-1), dict(n=0), dict(ldo=63), dict(codes=None), dict(scales=None), dict(out=None),
+    dict(fmt=-1), dict(dt=5), dict(rows=-1), dict(n=0), dict(ldo=63), dict(ldo=(1 << 32) + 1), dict(codes=None), dict(scales=None), dict(out=None),
     dict(g=None), dict(fmt=0), dict(codes=ODD), dict(scales=ODD), dict(out=ODD)])
 def test_dequantize_refusals(kw):
     assert dequantize(**kw) == BAD
@@ -70,6 +70,7 @@ def grouped(xc=P, xs=P, xg=P, off=P, E=4, wc=P, ws=P, wg=P, fmt=1, T=8, m=64, n=
 
 
 PRODUCT = [dict(fmt=2), dict(ydt=2), dict(T=-1), dict(m=0), dict(n=0), dict(n=BIG), dict(m=BIG, ldy=BIG), dict(ldy=63),
+           dict(ldy=(1 << 32) + 1),
            dict(wc=None), dict(ws=None), dict(y=None), dict(wg=None), dict(fmt=0), dict(wc=ODD), dict(ws=ODD), dict(y=ODD)]
 TOKENS = [dict(xc=None), dict(xs=None), dict(xg=None), dict(xc=ODD), dict(xs=ODD), dict(xg=ODD)]
 
@@ -97,8 +98,11 @@ def test_matvec_refusals(kw):
     assert b"fp4_matvec" in L.kronq_last_error()
 
 
-def test_matvec_token_limit():
+def test_limits():
     assert matvec(T=17) == UNSUP
+    n = (1 << 24) + 1
+    assert matvec(n=n, ldx=n) == UNSUP and matmul(n=n) == UNSUP and grouped(n=n) == UNSUP
+    assert matmul(T=1 << 29, m=1 << 29, ldy=1 << 29) == UNSUP
 
 
 def test_no_tokens_is_a_no_op():
