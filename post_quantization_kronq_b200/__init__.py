@@ -395,13 +395,19 @@ def _fp4_scale(t, name, fmt, count, device):
     return t.data_ptr()
 
 
-def _fp4_ws(ws, need, args, device):
-    """(pointer, bytes, owner) of the workspace; allocated where none is given and one is needed."""
+def _fp4_ws(ws, need, args, device, stream):
+    """(pointer, bytes, owner) of the workspace; allocated where none is given
+    and one is needed, on the call's stream, since it is freed before the
+    kernels there have run."""
     if ws is None:
         nbytes = need(*args)
         if nbytes == 0:
             return None, 0, None
-        ws = workspace(nbytes, device)
+        if stream is None:
+            ws = workspace(nbytes, device)
+        else:
+            with _torch.cuda.stream(stream):
+                ws = workspace(nbytes, device)
     elif ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous on {device}")
     return ws.data_ptr(), ws.nbytes, ws
@@ -435,7 +441,7 @@ def kronq_fp4_quantize(x, fmt: int, codes, scales, gscale=None, gscale_given: bo
             raise ValueError("deq must have x's shape, type and device")
     pw, nw = None, 0
     if pg is not None and not gscale_given:
-        pw, nw, ws = _fp4_ws(ws, kronq_fp4_quantize_workspace_bytes, (rows, n, fmt), dev)
+        pw, nw, ws = _fp4_ws(ws, kronq_fp4_quantize_workspace_bytes, (rows, n, fmt), dev, stream)
     _fp4_call(lib.kronq_fp4_quantize, dev, stream, px, _fp4_dtype(x), rows, n, ldx, fmt, pc, ps, pg,
               1 if gscale_given else 0, pd, ldd, pw, nw)
 
@@ -461,7 +467,7 @@ def kronq_fp4_matmul(xc, xs, wc, wsc, fmt: int, n: int, y, xg=None, wg=None, ws=
     pxc, pxs = _fp4_pair(xc, xs, "X", fmt, (T,), n, dev)
     pwc, pws = _fp4_pair(wc, wsc, "W", fmt, (m,), n, dev)
     pxg, pwg = _fp4_scale(xg, "xg", fmt, 1, dev), _fp4_scale(wg, "wg", fmt, 1, dev)
-    pw, nw, ws = _fp4_ws(ws, kronq_fp4_matmul_workspace_bytes, (T, m, n, fmt), dev)
+    pw, nw, ws = _fp4_ws(ws, kronq_fp4_matmul_workspace_bytes, (T, m, n, fmt), dev, stream)
     _fp4_call(lib.kronq_fp4_matmul, dev, stream, pxc, pxs, pxg, pwc, pws, pwg, fmt, T, m, n, py, _fp4_dtype(y),
               ldy, pw, nw)
 
@@ -480,7 +486,7 @@ def kronq_fp4_matvec(x, wc, wsc, fmt: int, y, wg=None, ws=None, stream=None):
         raise ValueError("x and y must have the same rows and device")
     pwc, pws = _fp4_pair(wc, wsc, "W", fmt, (m,), n, dev)
     pwg = _fp4_scale(wg, "wg", fmt, 1, dev)
-    pw, nw, ws = _fp4_ws(ws, kronq_fp4_matvec_workspace_bytes, (T, m, n, fmt), dev)
+    pw, nw, ws = _fp4_ws(ws, kronq_fp4_matvec_workspace_bytes, (T, m, n, fmt), dev, stream)
     _fp4_call(lib.kronq_fp4_matvec, dev, stream, px, _fp4_dtype(x), ldx, pwc, pws, pwg, fmt, T, m, n, py,
               _fp4_dtype(y), ldy, pw, nw)
 

@@ -319,6 +319,33 @@ def test_matvec_extreme_tokens(xdt):
         assert (np.abs(got[t] - y64[t]) <= tolerance(n, S[t], y64[t], torch.float32) + n * 2.0 ** -149).all()
 
 
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_matvec_nan_blocks_infinite_tokens_and_padding(fmt):
+    rng = np.random.default_rng(18)
+    n, m = 650, 90
+    wv = rng.standard_normal((m, n))
+    wv[7, 300], wv[11] = np.inf, 0.0
+    w = stored(wv, fmt)
+    nb = -(-n // fp4.BLOCK[fmt])
+    w[0][:, n // 2:] = 0x77                      # what lies behind the row's data may be anything
+    w[1][:, nb:] = 0xFF if fmt == MX else 0x7F
+    x = rng.standard_normal((3, n)).astype(np.float32)
+    x[1, 5] = np.inf
+    y = torch.empty(3, m, device=DEV)
+    kq.kronq_fp4_matvec(torch.from_numpy(x).to(DEV), w[0], w[1], fmt, y, wg=w[2])
+    y = y.cpu()
+    assert torch.isnan(y[:, 7]).all()
+    col = torch.from_numpy(w[3][:, 5])
+    for r in range(m):
+        if r != 7:   # infinity times the weight's sign, NaN for a zero weight
+            v = float(y[1, r])
+            assert np.isnan(v) if col[r] == 0 else v == np.sign(float(col[r])) * np.inf
+    rest = np.delete(np.arange(m), 7)
+    y64, S = fp4.product(x[[0, 2]], w[3][rest], None, g_of(w))
+    got = y.double().numpy()[[0, 2]][:, rest]
+    assert (np.abs(got - y64) <= tolerance(n, S, y64, torch.float32)).all()
+
+
 def test_matvec_strided_tokens_and_output():
     rng = np.random.default_rng(12)
     for fmt, n in ((NV, 333), (MX, 640)):
@@ -461,6 +488,35 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for job in jobs:
         assert torch.equal(job[5], job[4])
+
+
+def test_scratch_of_a_call_belongs_to_its_stream(monkeypatch):
+    """A workspace that a call allocates is freed when the call returns: on
+    another stream than the call's it could be handed out while in use."""
+    rng = np.random.default_rng(19)
+    T, m, n = 16, 256, 14336
+    x, w = stored(rng.standard_normal((T, n)), NV), stored(rng.standard_normal((m, n)), NV)
+    xf = torch.randn(T, n, device=DEV)
+    side, at, make = torch.cuda.Stream(), [], kq.workspace
+
+    def spy(nbytes, device="cuda"):
+        at.append(torch.cuda.current_stream().cuda_stream)
+        return make(nbytes, device)
+
+    want, y = torch.empty(2, T, m, device=DEV), torch.empty(2, T, m, device=DEV)
+    matmul(x, w, NV, n, want[0])
+    kq.kronq_fp4_matvec(xf, w[0], w[1], NV, want[1], wg=w[2])
+    torch.cuda.synchronize()
+    monkeypatch.setattr(kq, "workspace", spy)
+    g = torch.empty(1, device=DEV)
+    codes, scales = torch.empty_like(x[0]), torch.empty_like(x[1])
+    side.wait_stream(torch.cuda.current_stream())
+    matmul(x, w, NV, n, y[0], stream=side)
+    kq.kronq_fp4_matvec(xf, w[0], w[1], NV, y[1], wg=w[2], stream=side)
+    kq.kronq_fp4_quantize(xf, NV, codes, scales, gscale=g, stream=side)
+    assert at == [side.cuda_stream] * 3
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
 
 
 def test_repeats_are_bitwise_equal():
