@@ -27,7 +27,7 @@
 // PFLOP/s at 1.15 GHz, 0.85 and more of the tensor rate at that clock), by the
 // supply of operands and scales at full clocks, by HBM for few tokens (16 tokens,
 // 8192 x 28672 NVFP4 32 us, 0.62 of the measured rate with the columns split),
-// by latency below that (100 x 1000 x 4095 11 us).
+// by latency below that (100 x 1000 x 4095 9 us in four parts).
 //
 // The odd CTA's loaders arrive at the even CTA's barrier, whose MMA thread
 // copies the scales of both.  The arrival does not release at cluster scope
@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // y = the splits' partial sums in order, scaled.
 __global__ void __launch_bounds__(256) fp4_join_kernel(const GemmArgs a, int bf16) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = a.T * a.m;
+  fp4_await_first();
   if (i >= total) return;
   const float v = __fmul_rn(__fmul_rn(fp4_join(a.part + i, total, a.splits), a.xg ? *a.xg : 1.f), a.wg ? *a.wg : 1.f);
   const int64_t t = i / a.m, r = i - t * a.m;
@@ -607,17 +608,22 @@ __global__ void __launch_bounds__(256) fp4_join_kernel(const GemmArgs a, int bf1
 }
 
 // Chunks of a split.  The columns are split where the tiles would leave at
-// least half of the pairs of SMs idle, into as many parts as give each pair
-// at most one, of at least kSplitChunks chunks each (below that the launch
-// that joins them costs what the split saves).
-constexpr int64_t kSplitPairs = 74, kSplitChunks = 16;
+// least half of the pairs of SMs idle, into at most one part for each pair, as
+// the sum of three times decides: a chunk of a part 0.3 us (0.22 - 0.35
+// measured), the kernel that joins the parts 2.2 us, and the partial sums'
+// way to memory and back at 4.5 TB/s (256 tokens, 4096 x 4096 NVFP4: 14 us
+// whole, 18 in four parts; 100 tokens, 1000 x 4095: 11.0 and 9.0).
+constexpr int64_t kSplitPairs = 74;
 int64_t split_chunks(int64_t T, int64_t m, int64_t n) {
   const int64_t chunks = ceil_div(n, CK), tiles = ceil_div(m, GM) * ceil_div(T, GN);
   if (2 * tiles > kSplitPairs) return chunks;
-  int64_t parts = kSplitPairs / tiles;
-  if (parts > chunks / kSplitChunks) parts = chunks / kSplitChunks;
-  if (parts < 2) return chunks;
-  return ceil_div(ceil_div(chunks, parts), 4) * 4;   // whole loader groups
+  int64_t best = chunks, best_ns = 300 * chunks;
+  for (int64_t parts = 2; parts <= kSplitPairs / tiles; ++parts) {
+    const int64_t per = ceil_div(ceil_div(chunks, parts), 4) * 4;   // whole loader groups
+    const int64_t ns = 300 * per + 2200 + ceil_div(chunks, per) * T * m * 8 / 4500;
+    if (per < chunks && ns < best_ns) best = per, best_ns = ns;
+  }
+  return best;
 }
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const GemmArgs);
@@ -723,8 +729,12 @@ kronq_status fp4_gemm(const Fp4Gemm& g, int fmt, cudaStream_t s) {
     return cuda_fail(e, "fp4_gemm_kernel");
   }
   if (a.part) {
-    fp4_join_kernel<<<(unsigned)ceil_div(g.T * g.m, 256), 256, 0, s>>>(a, g.y_bf16);
-    KQ_LAUNCH_CHECK("fp4_join_kernel");
+    e = fp4_launch_second(fp4_join_kernel, (unsigned)ceil_div(g.T * g.m, 256), 256, s, a, g.y_bf16);
+    count_launch();
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return cuda_fail(e, "fp4_join_kernel");
+    }
   }
   return KRONQ_OK;
 }

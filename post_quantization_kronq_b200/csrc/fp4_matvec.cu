@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
 // y = the slices' partial sums in order, scaled.
 __global__ void __launch_bounds__(256) fp4_matvec_join_kernel(const VecArgs a, int slices) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = (int64_t)a.T * a.m;
+  fp4_await_first();
   if (i >= total) return;
   const float v = __fmul_rn(fp4_join(a.part + i, total, slices), a.wg ? *a.wg : 1.f);
   const int64_t tk = i / a.m, r = i - tk * a.m;
@@ -551,8 +552,12 @@ kronq_status fp4_matvec(const Fp4Matvec& v, int fmt, cudaStream_t st) {
   if (fmt == KRONQ_MXFP4) r = v.x_f32 ? launch_vec<KRONQ_MXFP4, true>(a, grid, smem, dev, st) : launch_vec<KRONQ_MXFP4, false>(a, grid, smem, dev, st);
   else r = v.x_f32 ? launch_vec<KRONQ_NVFP4, true>(a, grid, smem, dev, st) : launch_vec<KRONQ_NVFP4, false>(a, grid, smem, dev, st);
   if (r != KRONQ_OK || slices == 1) return r;
-  fp4_matvec_join_kernel<<<(unsigned)ceil_div(v.T * v.m, 256), 256, 0, st>>>(a, (int)slices);
-  KQ_LAUNCH_CHECK("fp4_matvec_join_kernel");
+  const cudaError_t e = fp4_launch_second(fp4_matvec_join_kernel, (unsigned)ceil_div(v.T * v.m, 256), 256, st, a, (int)slices);
+  count_launch();
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, "fp4_matvec_join_kernel");
+  }
   return KRONQ_OK;
 }
 

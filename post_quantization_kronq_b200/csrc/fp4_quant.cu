@@ -341,6 +341,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(QT, 4) fp4_amax_kernel(const QuantArgs a, uint32_t* partial) {
   constexpr int NW = BF16 ? 8 : 16;
   constexpr int RUNS = BF16 ? 2 * AMAX_RUNS : AMAX_RUNS;
+  fp4_let_next_in();
   float best = 0.f;
   const int64_t per = (a.n + 15) / 16, total = a.rows * per;
   const int lane = threadIdx.x & 31;
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(QT, 4) fp4_quantize_kernel(const QuantArgs a) 
   bool g_bad = false;
   if (FMT == KRONQ_NVFP4) {
     if (a.partial) {
+      fp4_await_first();
       __shared__ uint32_t red[QT / 32];
       uint32_t best = 0;
       for (int i = threadIdx.x; i < a.npartial; i += QT) best = max(best, a.partial[i]);
@@ -705,6 +707,16 @@ kronq_status kronq_fp4_quantize(const void* x, kronq_dtype dt, int64_t rows, int
     const int64_t units = rows * a.lds * (fmt == KRONQ_MXFP4 ? 2 : 1);
     const unsigned grid = quant_grid(units, 4);
     a.table = units >= 2 * (int64_t)grid * QT;
+    if (a.npartial) {
+      const cudaError_t e = dt == KRONQ_BF16 ? fp4_launch_second(fp4_quantize_kernel<KRONQ_NVFP4, true>, grid, QT, st, a)
+                                             : fp4_launch_second(fp4_quantize_kernel<KRONQ_NVFP4, false>, grid, QT, st, a);
+      count_launch();
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e, "fp4_quantize_kernel");
+      }
+      return KRONQ_OK;
+    }
     if (fmt == KRONQ_MXFP4) {
       if (dt == KRONQ_BF16) fp4_quantize_kernel<KRONQ_MXFP4, true><<<grid, QT, 0, st>>>(a);
       else fp4_quantize_kernel<KRONQ_MXFP4, false><<<grid, QT, 0, st>>>(a);

@@ -544,6 +544,20 @@ def test_matmul_with_split_columns(fmt, dt, T, m, n):
     assert (big[:, 0] == 9.0).all() and (big[:, -2:] == 9.0).all()
 
 
+@pytest.mark.parametrize("fmt, dt, T, m, n", [
+    (NV, torch.float32, 5, 64, 20000), (MX, torch.bfloat16, 300, 300, 8191), (NV, torch.bfloat16, 100, 1000, 4095),
+    (MX, torch.float32, 17, 1100, 4352)])
+def test_matmul_in_many_short_parts(fmt, dt, T, m, n):
+    parts = kq.kronq_fp4_matmul_workspace_bytes(T, m, n, fmt) // (T * m * 4)
+    assert parts >= 4
+    rng = np.random.default_rng(T + n + m)
+    x, w = stored(rng.standard_normal((T, n)), fmt), stored(0.02 * rng.standard_normal((m, n)), fmt)
+    out = torch.full((T + 1, m), 9.0, dtype=dt, device=DEV)
+    matmul(x, w, fmt, n, out[:T])
+    check(out[:T], *fp4.product(x[3], w[3], g_of(x), g_of(w)), n)
+    assert (out[T] == 9.0).all()
+
+
 @pytest.mark.parametrize("T", [1, 4, 11, 16])
 @pytest.mark.parametrize("xdt", [torch.bfloat16, torch.float32])
 def test_matvec_ranges_within_a_token(T, xdt):
