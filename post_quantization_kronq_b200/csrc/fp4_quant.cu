@@ -586,10 +586,13 @@ struct DequantArgs {
 
 // Each warp step takes UNROLL runs of 16 codes a lane, so that enough loads
 // are in flight: a run reads only 9 bytes for the 32 or 64 that it writes.
-constexpr int UNROLL = 4;
+// Where DQ_RUNS would leave SMs without a block, or with one where another's
+// stores would have covered its waits, one run: 100 x 4095 NVFP4 to float32
+// 5.2 -> 2.8 us, 1000 x 4095 8.0 -> 7.3, but 28672 x 8192 to bf16 104 -> 132.
+constexpr int DQ_RUNS = 4;
 
-template <int FMT, bool BF16, bool VEC>
-__global__ void __launch_bounds__(QT, 3) fp4_dequantize_kernel(const DequantArgs a) {
+template <int FMT, bool BF16, bool VEC, int UNROLL>
+__global__ void __launch_bounds__(QT, UNROLL == 1 ? 4 : 3) fp4_dequantize_kernel(const DequantArgs a) {
   const float g = FMT == KRONQ_NVFP4 ? *a.gscale : 1.f;
   const int64_t per = (a.n + 15) / 16;
   const int64_t total = a.rows * per;
@@ -750,15 +753,20 @@ kronq_status kronq_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, c
     a.ldc = fp4_code_row(n); a.lds = fp4_scale_row(fmt, n);
     a.gscale = gscale; a.out = out; a.ldo = ldo;
     const int vec_out = aligned(out, 32) && (ldo * esize) % 32 == 0;   // rows are 32-byte aligned
-    const unsigned grid = quant_grid(ceil_div(rows * ceil_div(n, 16), UNROLL), 6);
+    // aligned bf16 rows leave a block the least to store (2048 x 2048: 3.9 us
+    // with DQ_RUNS, 4.2 with one)
+    const int64_t runs = rows * ceil_div(n, 16);
+    const bool one = runs < (dt == KRONQ_BF16 && vec_out ? 1 : 2) * (int64_t)fp4_sms(nullptr) * QT * DQ_RUNS;
+    const unsigned grid = quant_grid(one ? runs : ceil_div(runs, DQ_RUNS), 6);
     cudaStream_t st = as_stream(s);
     using K = void (*)(const DequantArgs);
-    static const K kernels[8] = {
-        fp4_dequantize_kernel<KRONQ_MXFP4, false, false>, fp4_dequantize_kernel<KRONQ_MXFP4, false, true>,
-        fp4_dequantize_kernel<KRONQ_MXFP4, true, false>,  fp4_dequantize_kernel<KRONQ_MXFP4, true, true>,
-        fp4_dequantize_kernel<KRONQ_NVFP4, false, false>, fp4_dequantize_kernel<KRONQ_NVFP4, false, true>,
-        fp4_dequantize_kernel<KRONQ_NVFP4, true, false>,  fp4_dequantize_kernel<KRONQ_NVFP4, true, true>};
-    kernels[4 * (fmt == KRONQ_NVFP4) + 2 * (dt == KRONQ_BF16) + vec_out]<<<grid, QT, 0, st>>>(a);
+#define FP4_DQ(F, B) \
+  fp4_dequantize_kernel<F, B, false, DQ_RUNS>, fp4_dequantize_kernel<F, B, false, 1>, \
+  fp4_dequantize_kernel<F, B, true, DQ_RUNS>, fp4_dequantize_kernel<F, B, true, 1>
+    static const K kernels[16] = {FP4_DQ(KRONQ_MXFP4, false), FP4_DQ(KRONQ_MXFP4, true), FP4_DQ(KRONQ_NVFP4, false),
+                                  FP4_DQ(KRONQ_NVFP4, true)};
+#undef FP4_DQ
+    kernels[8 * (fmt == KRONQ_NVFP4) + 4 * (dt == KRONQ_BF16) + 2 * vec_out + one]<<<grid, QT, 0, st>>>(a);
     KQ_LAUNCH_CHECK("fp4_dequantize_kernel");
     return KRONQ_OK;
   });

@@ -171,6 +171,34 @@ def test_quantize_in_place_and_no_rows():
 
 @pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n,ld,first", [(1300, 4096, 4096, 0), (1300, 4099, 4099, 0), (1300, 4096, 4110, 3),
+                                             (190, 8192, 8192, 0), (2500, 2000, 2016, 0)])
+def test_dequantize_of_many_rows(fmt, dt, rows, n, ld, first):
+    """Sizes on both sides of the number of runs that a step takes, aligned and
+    unaligned rows; what lies between the rows stays."""
+    gen = torch.Generator(device=DEV).manual_seed(rows + n)
+    c, s = (torch.empty(rows, b, dtype=torch.uint8, device=DEV)
+            for b in (kq.kronq_fp4_code_row_bytes(n), kq.kronq_fp4_scale_row_bytes(fmt, n)))
+    c.random_(0, 256, generator=gen)
+    s.random_(100, 130, generator=gen) if fmt == MX else s.random_(0, 127, generator=gen)
+    g = torch.full((1,), 0.37, device=DEV) if fmt == NV else None
+    big = torch.full((rows, ld), 7.0, dtype=dt, device=DEV)
+    out = big[:, first:first + n]
+    kq.kronq_fp4_dequantize(c, s, fmt, out, gscale=g)
+    nib = torch.stack([c & 15, c >> 4], 2).reshape(rows, -1)[:, :n].long()
+    table = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], device=DEV)
+    value = torch.where(nib >= 8, -table[nib & 7], table[nib & 7])
+    sb = s.repeat_interleave(fp4.BLOCK[fmt], 1)[:, :n]
+    # a code times its scale is exact in float32, and one rounding for each of the scale and the type remains
+    scale = (sb.int() << 23).view(torch.float32) if fmt == MX else sb.view(torch.float8_e4m3fn).float()
+    want = value * scale if g is None else value * scale * g
+    assert torch.equal(out, want.to(dt))
+    big[:, first:first + n] = 7.0
+    assert (big == 7.0).all()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_dequantize_every_code_and_scale(fmt, dt):
     rng = np.random.default_rng(5)
     bs = fp4.BLOCK[fmt]
