@@ -53,9 +53,10 @@ kronq_status fp4_entry(F body) {
 // A call's second kernel need not wait to be launched until the first has
 // ended: it may begin when every block of the first has left or let it in, and
 // then waits for the first's end, its writes included, before it touches
-// memory.  Only a first kernel that fills every SM lets it in early (the
-// quantiser's; 6.9 -> 6.6 us for 7 x 4100): where some SMs have room, all of
-// the second's blocks gather on those (the products' joins got up to 1 us slower).
+// memory.  The quantiser's first pass lets the second in early (0.3 us of 5.5
+// for 16 x 4096, nothing from 500 x 4096 on).  The products do not: they leave
+// few SMs with room, all of a join's blocks gather on those, and it got up to
+// 1 us slower.
 __device__ __forceinline__ void fp4_let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void fp4_await_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>
