@@ -136,7 +136,7 @@ def _plain_quantize(x, fmt, g=None):
         scale = s * g.double()
         sbytes = s.float().to(torch.float8_e4m3fn).view(torch.uint8)
     y = torch.where(scale[:, :, None] > 0, b.abs() / scale[:, :, None], 0.0)
-    codes = _round_e2m1(y) + 8 * torch.signbit(b).to(torch.uint8)
+    codes = _round_e2m1(y) + 8 * torch.signbit(b)
     return codes.reshape(rows, -1)[:, :n], sbytes, g
 
 
