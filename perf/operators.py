@@ -251,22 +251,24 @@ def _run_own(st):
 
     case = st["case"]
     op, fmt = case["op"], case["fmt"]
-    if "ws" not in st:  # kept beside the state, as a layer keeps its own
+    if "ws" not in st:  # kept beside the state, as a layer keeps its own, with its weights' codes as bytes
         st["ws"] = kq.workspace(_workspace_bytes(kq, case), DEV)
+        st["wc"] = st["w"]["c"].to(torch.uint8) if "w" in st else None
     if op == "quantize":
         g = st["g"] if case["given"] else st["gout"]
         kq.kronq_fp4_quantize(st["x"], fmt, st["c"], st["s"], gscale=g, gscale_given=case["given"], deq=st["deq"], ws=st["ws"])
         return {"values": st["deq"], "tensor_scale": None if case["given"] else g}
+    # codes that the call is given anew are cast to the bytes it takes within the pass
     if op == "dequantize":
-        kq.kronq_fp4_dequantize(st["c"], st["s"], fmt, st["out"], gscale=st["g"])
+        kq.kronq_fp4_dequantize(st["c"].to(torch.uint8), st["s"], fmt, st["out"], gscale=st["g"])
         return st["out"]
-    x, w = st["x"], st["w"]
+    x, w, wc = st["x"], st["w"], st["wc"]
     if op == "matmul":
-        kq.kronq_fp4_matmul(x["c"], x["s"], w["c"], w["s"], fmt, case["n"], st["y"], xg=x["g"], wg=w["g"], ws=st["ws"])
+        kq.kronq_fp4_matmul(x["c"].to(torch.uint8), x["s"], wc, w["s"], fmt, case["n"], st["y"], xg=x["g"], wg=w["g"], ws=st["ws"])
     elif op == "matvec":
-        kq.kronq_fp4_matvec(x, w["c"], w["s"], fmt, st["y"], wg=w["g"], ws=st["ws"])
+        kq.kronq_fp4_matvec(x, wc, w["s"], fmt, st["y"], wg=w["g"], ws=st["ws"])
     else:
-        kq.kronq_fp4_grouped_matmul(x["c"], x["s"], st["offsets"], w["c"], w["s"], fmt, case["n"], st["y"], xg=x["g"], wg=w["g"])
+        kq.kronq_fp4_grouped_matmul(x["c"].to(torch.uint8), x["s"], st["offsets"], wc, w["s"], fmt, case["n"], st["y"], xg=x["g"], wg=w["g"])
     return st["y"]
 
 
