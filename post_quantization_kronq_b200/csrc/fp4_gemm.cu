@@ -29,11 +29,14 @@
 // 8192 x 28672 NVFP4 32 us, 0.62 of the measured rate with the columns split),
 // by latency below that (100 x 1000 x 4095 9 us in four parts).
 //
-// The odd CTA's loaders arrive at the even CTA's barrier, whose MMA thread
-// copies the scales of both.  The arrival does not release at cluster scope
-// (that takes 1500 - 2200 cycles): what it announces is read by the async
-// proxy of the writer's own CTA, and each writer's proxy fence has made it
-// visible there before the arrival is issued.
+// The loaders of both CTAs arrive at the even CTA's barrier, whose MMA thread
+// copies the scales of both.  Each loader's stores go behind a proxy fence (the
+// copies read by the async proxy) and a release at cluster scope that is
+// restricted to the CTA's own shared memory, and the MMA thread acquires at the
+// same scope.  An unrestricted release also waits for the loader's global loads in
+// flight (1500 - 2200 cycles), and from a warp without any, which hands the
+// arrivals on, it still made products 20 - 35 % slower.  The epilogue's
+// arrival orders reads of TMEM alone: the tcgen05 fences around it do that.
 //
 // Warps: 0 TMA, 1 MMA (one lane of the even CTA), 2-7 scales, 8-15 epilogue.
 #include <cuda.h>
@@ -182,12 +185,28 @@ __device__ __forceinline__ bool elect_lane() {
   return p != 0;
 }
 
-// Arrival at a barrier of the pair's even CTA without a release at cluster
-// scope: no generic write is handed over to the other CTA's threads (the
-// accumulator's columns have been read by tcgen05.ld; scale atoms are read by
-// the async proxy of the CTA that wrote them, behind its proxy fence).
+// Arrival at a barrier of the pair's even CTA.  Relaxed: what it announces is
+// ordered by a fence before it and one behind the wait, lighter ones than a
+// release and an acquire of all memory.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_remote(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// This CTA's shared memory to the pair's other CTA, and the other side.
+__device__ __forceinline__ void fence_release_smem() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void fence_acquire_smem() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 
 // D (+)= A B for the pair; alo, blo, hi: words of the operands' descriptors.
@@ -227,6 +246,13 @@ __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, volatile in
   if (mbar_wait(bar, parity)) return true;
   *abort_s = 1;
   return false;
+}
+
+// The same at a barrier that mbar_arrive_remote arrives at.
+__device__ __forceinline__ bool await_remote(uint32_t bar, uint32_t parity, volatile int* abort_s) {
+  while (!mbar_try_wait_remote(bar, parity))
+    if (!await(bar, parity, abort_s)) return false;
+  return true;
 }
 
 // Bytes of word j of a 16-byte piece of which `valid` bytes are data.
@@ -355,20 +381,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int count = t.c1 - t.c0;
         const uint32_t two = t.cols > GH ? 1u : 0u;
         const uint32_t idesc = fp4_idesc<FMT>(t.cols, 0);
-        ok = await(sffull0 + 8 * slot, sph, abort_s);
+        ok = await_remote(sffull0 + 8 * slot, sph, abort_s);
         if (!ok) break;
+        fence_acquire_smem();
         tc_fence_after();
         issued = true;
 #pragma unroll
         for (int i = 0; i < CH; ++i) copy_scales(i, buf, two);
         scales_done();
-        if (done_tiles > 0) ok = await(accempty, (done_tiles - 1) & 1, abort_s);
+        if (done_tiles > 0) ok = await_remote(accempty, (done_tiles - 1) & 1, abort_s);
         tc_fence_after();
         for (int lc = 0; ok && lc < count; lc += CH) {
           const bool more = lc + CH < count;
           if (more) {
-            ok = await(sffull0 + 8 * slot, sph, abort_s);
+            ok = await_remote(sffull0 + 8 * slot, sph, abort_s);
             if (!ok) break;
+            fence_acquire_smem();
             tc_fence_after();
           }
 #pragma unroll
@@ -485,6 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           fence_proxy_async_smem();
         }
         __syncwarp();
+        fence_release_smem();
         if (lane == 0) mbar_arrive_remote(lead + 8 * slot);
         if (++slot == SLOTS) { slot = 0; sph ^= 1; }
         valid[d] = issue(w);

@@ -1,0 +1,54 @@
+"""The 4-bit products on whole numbers: codes, and scales that are powers of two,
+whose sums are whole multiples of a unit and fit float32's 24 bits in any order,
+so that the products have to be equal to the float64 ones.  One code, scale or
+column that is left out, taken twice or misplaced shows."""
+import numpy as np
+import pytest
+import torch
+
+import post_quantization_kronq_b200 as kq
+from oracle import fp4
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+MX, NV = kq.MXFP4, kq.NVFP4
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def whole(rng, rows, n, fmt):
+    """(codes, scales, tensor scale, float64 values on the device): any code under scales of 2^-1 .. 2^1, another
+    one in every block."""
+    codes = rng.integers(0, 16, size=(rows, n)).astype(np.uint8)
+    e = rng.integers(-1, 2, size=(rows, -(-n // fp4.BLOCK[fmt])))
+    sb = ((127 + e) if fmt == MX else (7 + e) * 8).astype(np.uint8)
+    c, s = fp4.store(codes, sb, fmt)
+    return dev(c), dev(s), None if fmt == MX else torch.ones(1, device=DEV), dev(fp4.values(codes, sb, fmt))
+
+
+def product(x, w):
+    """X W^T in float64; values are multiples of 2^-2, so partial sums fit where sum |x w| is below 2^20."""
+    assert float((x.abs() @ w.abs().T).max()) < 2.0 ** 20
+    return x @ w.T
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("T,m,n", [(256, 512, 28672), (300, 700, 8192), (2048, 4096, 4096)])
+def test_scales_of_both_halves_of_a_pair_in_every_repeat(fmt, T, m, n):
+    """Rows 0 - 127 and 128 - 255 of a tile of W, and halves of its tokens, come
+    by way of two SMs; one of them multiplies.  Long rows, so that every slot
+    of scales is filled many times over, and many repeats."""
+    rng = np.random.default_rng(n)
+    x, w = whole(rng, T, n, fmt), whole(rng, m, n, fmt)
+    want = product(x[3], w[3])
+    y = torch.empty(T, m, device=DEV)
+    ws = kq.workspace(kq.kronq_fp4_matmul_workspace_bytes(T, m, n, fmt), DEV)
+    wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(60):
+        y.fill_(float("nan"))
+        kq.kronq_fp4_matmul(x[0], x[1], w[0], w[1], fmt, n, y, xg=x[2], wg=w[2], ws=ws)
+        wrong += (y != want).sum()
+    assert int(wrong) == 0
+    assert kq.kronq_device_status() == 0
