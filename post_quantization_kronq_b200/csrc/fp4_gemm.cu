@@ -261,6 +261,13 @@ __device__ __forceinline__ uint32_t tail_mask(int valid, int j) {
   return left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
 }
 
+// Both tensor scales as factors of a sum: their product and 1, unless the
+// product leaves float32's normal range.
+__device__ __forceinline__ float2 tensor_scales(const GemmArgs& a, int e) {
+  const float xg = a.xg ? *a.xg : 1.f, wg = a.wg ? a.wg[e] : 1.f, both = __fmul_rn(xg, wg);
+  return both >= 1.17549435e-38f && both <= 3.40282347e38f ? make_float2(both, 1.f) : make_float2(xg, wg);
+}
+
 template <int FMT, bool BF16, bool PART>
 __global__ void __launch_bounds__(THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
@@ -529,11 +536,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!__shfl_sync(0xffffffffu, good, 0)) break;
       tc_fence_after();
       const int64_t r = t.m0 + GH * (int64_t)rank + q * 32 + lane;
-      // both tensor scales as one factor, unless their product leaves float32's normal range
-      float xg = !PART && a.xg ? *a.xg : 1.f, wg = !PART && a.wg ? a.wg[t.e] : 1.f;
-      const float both = __fmul_rn(xg, wg);
-      const bool one = PART || (both >= 1.17549435e-38f && both <= 3.40282347e38f);
-      if (one) xg = both;
+      const float2 scale = PART ? make_float2(1.f, 1.f) : tensor_scales(a, t.e);
+      const float xg = scale.x, wg = scale.y;
+      const bool one = wg == 1.f;
       const int groups = t.cols / 64;    // 32-column groups of this warp: half, half + 2, ...
       const int64_t ld = PART ? a.m : a.ldy;
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -630,7 +635,8 @@ __global__ void __launch_bounds__(256) fp4_join_kernel(const GemmArgs a, int bf1
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = a.T * a.m;
   fp4_await_first();
   if (i >= total) return;
-  const float v = __fmul_rn(__fmul_rn(fp4_join(a.part + i, total, a.splits), a.xg ? *a.xg : 1.f), a.wg ? *a.wg : 1.f);
+  const float2 scale = tensor_scales(a, 0);
+  const float v = __fmul_rn(__fmul_rn(fp4_join(a.part + i, total, a.splits), scale.x), scale.y);
   const int64_t t = i / a.m, r = i - t * a.m;
   if (bf16) static_cast<__nv_bfloat16*>(a.y)[t * a.ldy + r] = __float2bfloat16_rn(v);
   else static_cast<float*>(a.y)[t * a.ldy + r] = v;

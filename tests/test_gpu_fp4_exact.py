@@ -52,3 +52,19 @@ def test_scales_of_both_halves_of_a_pair_in_every_repeat(fmt, T, m, n):
         wrong += (y != want).sum()
     assert int(wrong) == 0
     assert kq.kronq_device_status() == 0
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,m,n,split", [(100, 1000, 4095, True), (16, 300, 20000, True), (300, 5000, 512, False)])
+def test_tensor_scales_far_apart(dt, T, m, n, split):
+    """Tensor scales whose product is an ordinary number count as that number,
+    also where a sum times one of them would leave float32's range."""
+    rng = np.random.default_rng(T)
+    x, w = whole(rng, T, n, NV), whole(rng, m, n, NV)
+    assert (kq.kronq_fp4_matmul_workspace_bytes(T, m, n, NV) > 0) == split
+    one, y = (torch.empty(T, m, dtype=dt, device=DEV) for _ in range(2))
+    kq.kronq_fp4_matmul(x[0], x[1], w[0], w[1], NV, n, one, xg=x[2], wg=w[2])
+    for a, b in ((-126, 100), (100, -126), (120, -100), (-100, 120)):
+        ga, gb = torch.tensor([2.0 ** a], device=DEV), torch.tensor([2.0 ** b], device=DEV)
+        kq.kronq_fp4_matmul(x[0], x[1], w[0], w[1], NV, n, y, xg=ga, wg=gb)
+        assert torch.equal(y, one * 2.0 ** (a + b))
