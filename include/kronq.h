@@ -515,7 +515,8 @@ kronq_status kronq_fp4_matmul(const uint8_t* xc, const uint8_t* xs, const float*
  * tokens X (T x n, bf16 or float32, row stride ldx) that are not quantised
  * (single-token decode with 4-bit weights).  Weights and bf16 tokens enter the
  * products exactly, float32 tokens to 2^-22 of each value or better; sums in
- * float32, in an order that depends on the sizes alone.  n at most 2^24.
+ * float32; a result's order depends on the sizes and types, its token and its
+ * row of W alone.  n at most 2^24.
  * Other arguments as kronq_fp4_matmul. */
 size_t kronq_fp4_matvec_workspace_bytes(int64_t T, int64_t m, int64_t n, kronq_fp4_format fmt);
 kronq_status kronq_fp4_matvec(const void* x, kronq_dtype xdt, int64_t ldx, const uint8_t* wc, const uint8_t* ws,

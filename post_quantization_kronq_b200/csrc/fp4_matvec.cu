@@ -25,9 +25,11 @@
 // that brings its largest magnitude to [2^14, 2^15): bf16 values down to
 // 2^-31 of it are exact; a float32 value is two parts of 11 bits (2^-23 off
 // at most) down to 2^-28 of it.  The sum over a span is scaled back when it
-// joins the float32 sum of the row.  Spans that this does not cover (a wider
-// range within 128 columns, infinities and NaN, E8M0 scales beyond the range)
-// are computed in float32, one weight and token at a time.
+// joins the float32 sum of the row.  What this does not cover is computed in
+// float32, one weight and token at a time: a token's span with a wider range
+// within its 128 columns, infinities or NaN, and a block whose E8M0 scale is
+// beyond the range.  The mma sees zeros there, so that neither the other tokens
+// of a call nor the other rows of a tile are summed in another order.
 //
 // The order of k inside an mma is free as long as weights and tokens agree:
 // lane t of a span holds k = 32 t + 8 j + {0..7} as word j.  Tokens are staged
@@ -98,6 +100,9 @@ template <int FMT, bool XF32, int NT>
 struct Vec {
   static constexpr int PARTS = XF32 ? 2 : 1;
   static constexpr int BPL = FMT == KRONQ_NVFP4 ? 2 : 1;   // scale blocks of a lane's 32 columns
+  // spans of a step that are multiplied together, so that four chains of mma
+  // are in flight and the registers suffice
+  static constexpr int AT_ONCE = NT * PARTS >= 4 ? 1 : PAIR;
 
   struct Load {
     uint4 w[2];
@@ -164,8 +169,12 @@ struct Vec {
     return v;
   }
 
+  // Whether an E8M0 scale is beyond what fp16 takes.
+  static __device__ __forceinline__ bool beyond(uint32_t byte) { return byte < kMxLow || byte > kMxHigh; }
+
   // Multipliers of the lane's blocks, of which `left` columns are there (the
-  // others count as zero); true where one is beyond what fp16 takes.
+  // others count as zero, and so does a block that fp16 does not take); true
+  // where there is one of those.
   template <bool WHOLE>
   static __device__ __forceinline__ bool multipliers(const Load& v, int left, uint32_t (&mul)[2][BPL]) {
     bool odd = false;
@@ -178,104 +187,125 @@ struct Vec {
         mul[h][0] = __byte_perm(f, f, 0x1010);
         mul[h][BPL - 1] = __byte_perm(f, f, 0x3232);
       } else {
-        const bool in = WHOLE || left > 0;
-        odd |= in && (v.s[h] < kMxLow || v.s[h] > kMxHigh);
+        const bool in = WHOLE || left > 0, off = beyond(v.s[h]);
+        odd |= in && off;
         // fp16 2^(byte - 127 + 12), subnormal below 2^-14
         const int e = (int)v.s[h] - 127 + kMxShift + 15;
         const uint32_t one = e >= 1 ? (uint32_t)e << 10 : 1024u >> (1 - e);
-        mul[h][0] = in ? one | (one << 16) : 0u;
+        mul[h][0] = in && !off ? one | (one << 16) : 0u;
       }
     }
     return odd;
   }
 
-  // acc += the products of a step's spans; left: columns of the slice from the
+  // acc += the products of a step's spans in `slot`; left: columns of the slice from the
   // lane's first on (WHOLE: both spans are there); xs: its first piece of the tokens there (row stride of a token
   // and part a.xrow); fac: the factors of the lane's two tokens there; xnext,
-  // fnext: offsets of the second span's.
+  // fnext: offsets of the second span's; apart: the tokens of each span that
+  // fp16 does not cover, a bit each.
+  //
+  // What fp16 does not cover is zero in the mma and added behind it, token by
+  // token and block by block, so that a sum's order does not depend on the
+  // other tokens and rows.
   template <bool WHOLE>
-  static __device__ __forceinline__ void step(const VecArgs& a, const Load (&v)[PAIR], int left, const uint8_t* const (&xs)[NT], int xnext, const float* fac, int fnext,
-                                              bool plain, int64_t kend, int lane, float (&acc)[NT][4]) {
-    uint32_t mul[PAIR][2][BPL];
-    bool odd = plain;
+  static __device__ __forceinline__ void step(const VecArgs& a, const uint8_t* slot, int left, const uint8_t* const (&xs)[NT], int xnext, const float* fac, int fnext,
+                                              uint32_t apart0, uint32_t apart1, int64_t kend, int lane, float (&acc)[NT][4]) {
+    bool odd = false;
+    // no token left for the mma (looked at for few tokens, where it is likely: one token whose spans are all
+    // wide 166 -> 142 us, but 16 float32 tokens that are not 119 -> 125)
+    const bool none = NT == 1 && (apart0 & apart1) == (1u << a.T) - 1u;
 #pragma unroll
-    for (int s = 0; s < PAIR; ++s) odd |= multipliers<WHOLE>(v[s], left - s * SPAN, mul[s]);
-    if (FMT == KRONQ_MXFP4 ? __any_sync(0xffffffffu, odd) : plain) {
+    for (int s0 = 0; s0 < PAIR && !none; s0 += AT_ONCE) {
+      Load v[AT_ONCE];
+      uint32_t mul[AT_ONCE][2][BPL];
 #pragma unroll
-      for (int s = 0; s < PAIR; ++s) scalar(a, v[s], kend - left + s * SPAN, kend, lane, acc);
-      return;
-    }
-    float sum[PAIR][NT][PARTS][4] = {};
+      for (int s = 0; s < AT_ONCE; ++s) {
+        v[s] = take(slot + (s0 + s) * RSLOT, lane);
+        odd |= multipliers<WHOLE>(v[s], left - (s0 + s) * SPAN, mul[s]);
+      }
+      float sum[AT_ONCE][NT][PARTS][4] = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-      for (int s = 0; s < PAIR; ++s) {
-        uint32_t p[2][4];
+        for (int s = 0; s < AT_ONCE; ++s) {
+          uint32_t p[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          codes_f16(j == 0 ? v[s].w[h].x : j == 1 ? v[s].w[h].y : j == 2 ? v[s].w[h].z : v[s].w[h].w, p[h]);
+          for (int h = 0; h < 2; ++h) {
+            codes_f16(j == 0 ? v[s].w[h].x : j == 1 ? v[s].w[h].y : j == 2 ? v[s].w[h].z : v[s].w[h].w, p[h]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[h][i] = mul_f16x2(p[h][i], mul[s][h][BPL == 2 ? j >> 1 : 0]);
-        }
-        // registers: rows g, g + 8 at the first k pair, then at the second
-        const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
-        const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int q = 0; q < PARTS; ++q) {
-            const uint4 x = *reinterpret_cast<const uint4*>(xs[nt] + s * xnext + q * a.xrow + j * 64);
-            mma_16816(sum[s][nt][q], a0, x.x, x.y);
-            mma_16816(sum[s][nt][q], a1, x.z, x.w);
+            for (int i = 0; i < 4; ++i) p[h][i] = mul_f16x2(p[h][i], mul[s][h][BPL == 2 ? j >> 1 : 0]);
           }
-      }
-    }
+          // registers: rows g, g + 8 at the first k pair, then at the second
+          const uint32_t a0[4] = {p[0][0], p[1][0], p[0][1], p[1][1]};
+          const uint32_t a1[4] = {p[0][2], p[1][2], p[0][3], p[1][3]};
 #pragma unroll
-    for (int s = 0; s < PAIR; ++s)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float2 f = *reinterpret_cast<const float2*>(fac + s * fnext + 8 * nt);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float w = sum[s][nt][0][e];
-          if (XF32) w = fmaf(sum[s][nt][PARTS - 1][e], 0x1p-11f, w);
-          acc[nt][e] = fmaf(w, (e & 1) ? f.y : f.x, acc[nt][e]);
+            for (int q = 0; q < PARTS; ++q) {
+              const uint4 x = *reinterpret_cast<const uint4*>(xs[nt] + (s0 + s) * xnext + q * a.xrow + j * 64);
+              mma_16816(sum[s][nt][q], a0, x.x, x.y);
+              mma_16816(sum[s][nt][q], a1, x.z, x.w);
+            }
         }
       }
+#pragma unroll
+      for (int s = 0; s < AT_ONCE; ++s)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float2 f = *reinterpret_cast<const float2*>(fac + (s0 + s) * fnext + 8 * nt);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float w = sum[s][nt][0][e];
+            if (XF32) w = fmaf(sum[s][nt][PARTS - 1][e], 0x1p-11f, w);
+            acc[nt][e] = fmaf(w, (e & 1) ? f.y : f.x, acc[nt][e]);
+          }
+        }
+    }
+    if ((apart0 | apart1) != 0 || (FMT == KRONQ_MXFP4 && __any_sync(0xffffffffu, odd))) {
+#pragma unroll 1
+      for (int s = 0; s < PAIR; ++s) singly(a, slot + s * RSLOT, left - s * SPAN, kend, s ? apart1 : apart0, lane, acc);
+    }
   }
 
-  // The same sums in float32 from the tokens as given.
-  static __device__ __forceinline__ void scalar(const VecArgs& a, const Load& v, int64_t k, int64_t kend, int lane, float (&acc)[NT][4]) {
+  // A span's products that fp16 does not cover, in float32 from the tokens as
+  // given: all of the tokens in `apart`, and every token's with blocks whose
+  // scale is beyond its range.
+  static __device__ __forceinline__ void singly(const VecArgs& a, const uint8_t* slot, int left, int64_t kend, uint32_t apart, int lane, float (&acc)[NT][4]) {
+    const Load v = take(slot, lane);
     const int t = lane & 3;
+    uint32_t who[2];   // lanes with such a block, of the rows g and g + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) who[h] = __ballot_sync(0xffffffffu, FMT == KRONQ_MXFP4 && left > 0 && beyond(v.s[h]));
 #pragma unroll 1
     for (int tk = 0; tk < a.T; ++tk) {
+      const bool all = (apart >> tk) & 1u;
+      if (!all && !(who[0] | who[1])) continue;
       float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t w[4] = {v.w[h].x, v.w[h].y, v.w[h].z, v.w[h].w};
+        if (all || (who[h] >> lane & 1u)) {
+          const uint32_t w[4] = {v.w[h].x, v.w[h].y, v.w[h].z, v.w[h].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t b = BPL == 2 ? (v.s[h] >> (8 * (j >> 1))) & 0xFFu : v.s[h];
-          const float sc = fp4_scale_value<FMT>(b);
+          for (int j = 0; j < 4; ++j) {
+            const float sc = fp4_scale_value<FMT>(BPL == 2 ? (v.s[h] >> (8 * (j >> 1))) & 0xFFu : v.s[h]);
+            const int64_t at = tk * a.ldx + kend - left + 8 * j;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const float2 d = e2m1x2_float2((w[j] >> (8 * i)) & 0xFFu);
-            const int64_t at = k + 8 * j + 2 * i;
-            if (at < kend) s[h] = fmaf(d.x * sc, x_at(a, XF32, tk * a.ldx + at), s[h]);
-            if (at + 1 < kend) s[h] = fmaf(d.y * sc, x_at(a, XF32, tk * a.ldx + at + 1), s[h]);
+            for (int i = 0; i < 8; i += 2) {
+              const float2 d = e2m1x2_float2((w[j] >> (4 * i)) & 0xFFu);
+              if (8 * j + i < left) s[h] = fmaf(d.x * sc, x_at(a, XF32, at + i), s[h]);
+              if (8 * j + i + 1 < left) s[h] = fmaf(d.y * sc, x_at(a, XF32, at + i + 1), s[h]);
+            }
           }
         }
         s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
         s[h] += __shfl_xor_sync(0xffffffffu, s[h], 2);
       }
+      // who >> (lane & 28): the four lanes of a row
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        if (nt == (tk >> 3) && t == ((tk & 7) >> 1)) {
-          acc[nt][0] += (tk & 1) ? 0.f : s[0];
-          acc[nt][1] += (tk & 1) ? s[0] : 0.f;
-          acc[nt][2] += (tk & 1) ? 0.f : s[1];
-          acc[nt][3] += (tk & 1) ? s[1] : 0.f;
-        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (tk == 8 * nt + 2 * t + (e & 1) && (all || (who[e >> 1] >> (lane & 28) & 15u))) acc[nt][e] += s[e >> 1];
     }
   }
 };
@@ -328,10 +358,10 @@ __device__ __forceinline__ bool stage_span(const float (&f)[4], uint8_t* dst, in
 }
 
 template <int FMT, bool XF32, int NT>
-__global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
+__global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const __grid_constant__ VecArgs a) {
   using V = Vec<FMT, XF32, NT>;
   // the warps' rings, the tokens' parts, then per span the factors of 8 NT
-  // tokens and whether the span is computed in float32
+  // tokens and a bit for each token that is computed in float32 there
   extern __shared__ __align__(16) uint8_t xsm[];
   __shared__ float red[2][VW][16 * 8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -344,7 +374,7 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
   uint8_t* ring = xsm + warp * (RING * PAIR * RSLOT);
   uint8_t* xpart = xsm + RBYTES;
   float* fac = reinterpret_cast<float*>(xpart + (int64_t)a.T * V::PARTS * a.xrow);
-  int* plain = reinterpret_cast<int*>(fac + spans * 8 * NT);
+  uint32_t* apart = reinterpret_cast<uint32_t*>(fac + spans * 8 * NT);
 
   // the copies' position: RING - 1 steps ahead of the arithmetic's
   const int whole = cols / SPAN;                            // spans without a ragged end
@@ -375,7 +405,7 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
 #pragma unroll 1
   for (int i = 0; i < RING - 1; ++i) copy_next();
 
-  for (int i = threadIdx.x; i < spans * (8 * NT + 1); i += VT) fac[i] = 0.f;   // and plain
+  for (int i = threadIdx.x; i < spans * (8 * NT + 1); i += VT) fac[i] = 0.f;   // and apart
   __syncthreads();
   // a warp per span and token, four of them in flight
   for (int u0 = warp; u0 < spans * a.T; u0 += 4 * VW) {
@@ -408,7 +438,7 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
             f[w], xpart + (int64_t)tk * V::PARTS * a.xrow + x_offset(sp * SPAN + 4 * lane), a.xrow, factor);
         if (lane == 0) {
           fac[sp * 8 * NT + tk] = factor;
-          if (!covered) plain[sp] = 1;
+          if (!covered) atomicOr(&apart[sp], 1u << tk);
         }
       }
     }
@@ -434,17 +464,14 @@ __global__ void __launch_bounds__(VT, CTAS) fp4_matvec_kernel(const VecArgs a) {
         const uint8_t* xp[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) xp[nt] = xs[nt] + sp * 256;
-        typename V::Load v[PAIR];
-#pragma unroll
-        for (int s = 0; s < PAIR; ++s) v[s] = V::take(held + s * RSLOT, lane);
         const float* fp = fac + sp * 8 * NT + 2 * t;
         const int left = cols - sp * SPAN - 32 * t;
         if (sp + PAIR <= whole) {
-          V::template step<true>(a, v, left, xp, 256, fp, 8 * NT, (plain[sp] | plain[sp + 1]) != 0, k0 + cols, lane, acc);
+          V::template step<true>(a, held, left, xp, 256, fp, 8 * NT, apart[sp], apart[sp + 1], k0 + cols, lane, acc);
         } else {
           // a second span beyond the last has zero weights: any tokens do
           const int has = sp + 1 < spans ? 1 : 0;
-          V::template step<false>(a, v, left, xp, has * 256, fp, has * 8 * NT, (plain[sp] | plain[sp + has]) != 0,
+          V::template step<false>(a, held, left, xp, has * 256, fp, has * 8 * NT, apart[sp], has ? apart[sp + 1] : 0u,
                                   k0 + cols, lane, acc);
         }
         held += PAIR * RSLOT;
@@ -488,7 +515,7 @@ __global__ void __launch_bounds__(256) fp4_matvec_join_kernel(const VecArgs a, i
   else static_cast<float*>(a.y)[tk * a.ldy + r] = v;
 }
 
-// Shared memory of a span's factors and its float32 flag.
+// Shared memory of a span's factors and its float32 tokens.
 int span_bytes(int64_t T) { return (T > 8 ? 17 : 9) * 4; }
 
 // Columns of a slice: as many as leave room for the tokens' parts, fewer
