@@ -169,8 +169,12 @@ struct Vec {
     return v;
   }
 
-  // Whether an E8M0 scale is beyond what fp16 takes.
+  // Whether fp16 does not take an E8M0 scale, and whether that matters: it does
+  // not for zeros (a block of zeros has the lowest scale), except under NaN.
   static __device__ __forceinline__ bool beyond(uint32_t byte) { return byte < kMxLow || byte > kMxHigh; }
+  static __device__ __forceinline__ bool counts(uint32_t byte, const uint4& w) {
+    return ((w.x | w.y | w.z | w.w) & 0x77777777u) != 0 || byte == 255u;
+  }
 
   // Multipliers of the lane's blocks, of which `left` columns are there (the
   // others count as zero, and so does a block that fp16 does not take); true
@@ -275,7 +279,8 @@ struct Vec {
     const int t = lane & 3;
     uint32_t who[2];   // lanes with such a block, of the rows g and g + 8
 #pragma unroll
-    for (int h = 0; h < 2; ++h) who[h] = __ballot_sync(0xffffffffu, FMT == KRONQ_MXFP4 && left > 0 && beyond(v.s[h]));
+    for (int h = 0; h < 2; ++h) who[h] = __ballot_sync(0xffffffffu, FMT == KRONQ_MXFP4 && left > 0 && beyond(v.s[h]) && counts(v.s[h], v.w[h]));
+    if (!(apart | who[0] | who[1])) return;
 #pragma unroll 1
     for (int tk = 0; tk < a.T; ++tk) {
       const bool all = (apart >> tk) & 1u;
