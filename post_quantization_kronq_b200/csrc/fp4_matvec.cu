@@ -289,10 +289,12 @@ struct Vec {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (all || (who[h] >> lane & 1u)) {
+          // 4 * 2^126 and more is beyond float32: a block under the highest scales is summed at an eighth
+          const bool high = FMT == KRONQ_MXFP4 && v.s[h] >= 253u && v.s[h] != 255u;
           const uint32_t w[4] = {v.w[h].x, v.w[h].y, v.w[h].z, v.w[h].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float sc = fp4_scale_value<FMT>(BPL == 2 ? (v.s[h] >> (8 * (j >> 1))) & 0xFFu : v.s[h]);
+            const float sc = fp4_scale_value<FMT>(BPL == 2 ? (v.s[h] >> (8 * (j >> 1))) & 0xFFu : high ? v.s[h] - 3u : v.s[h]);
             const int64_t at = tk * a.ldx + kend - left + 8 * j;
 #pragma unroll 1
             for (int i = 0; i < 8; i += 2) {
@@ -301,6 +303,7 @@ struct Vec {
               if (8 * j + i + 1 < left) s[h] = fmaf(d.y * sc, x_at(a, XF32, at + i + 1), s[h]);
             }
           }
+          if (high) s[h] *= 8.f;
         }
         s[h] += __shfl_xor_sync(0xffffffffu, s[h], 1);
         s[h] += __shfl_xor_sync(0xffffffffu, s[h], 2);

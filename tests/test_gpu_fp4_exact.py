@@ -68,3 +68,20 @@ def test_tensor_scales_far_apart(dt, T, m, n, split):
         ga, gb = torch.tensor([2.0 ** a], device=DEV), torch.tensor([2.0 ** b], device=DEV)
         kq.kronq_fp4_matmul(x[0], x[1], w[0], w[1], NV, n, y, xg=ga, wg=gb)
         assert torch.equal(y, one * 2.0 ** (a + b))
+
+
+@pytest.mark.parametrize("T,m,n", [(130, 300, 1056), (20, 200, 8192)])
+def test_e8m0_scales_at_the_ends(T, m, n):
+    """Scales from 2^-127 to 2^127, those of tokens against those of weights:
+    their product is 1 in every block, and the sums are whole."""
+    rng = np.random.default_rng(n)
+    xc, wc = (rng.integers(0, 16, size=(r, n)).astype(np.uint8) for r in (T, m))
+    e = rng.integers(0, 255, size=(1, -(-n // 32)))
+    e[0, :4] = 0, 254, 1, 253
+    xq = fp4.store(xc, np.repeat(e, T, 0).astype(np.uint8), MX)
+    wq = fp4.store(wc, np.repeat(254 - e, m, 0).astype(np.uint8), MX)
+    one = np.full((1, e.shape[1]), 127, np.uint8)
+    want = product(*(dev(fp4.values(c, np.repeat(one, len(c), 0), MX)) for c in (xc, wc)))
+    y = torch.empty(T, m, device=DEV)
+    kq.kronq_fp4_matmul(dev(xq[0]), dev(xq[1]), dev(wq[0]), dev(wq[1]), MX, n, y)
+    assert torch.equal(y.double(), want)

@@ -116,3 +116,26 @@ def test_blocks_of_zeros_cost_no_more_than_others(T):
             t.append(a.elapsed_time(b))
     dense, zeros = (sorted(t)[4] for t in times)
     assert zeros < 1.5 * dense
+
+
+@pytest.mark.parametrize("xdt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [1, 3, 16])
+@pytest.mark.parametrize("byte", [0, 1, 60, 200, 251, 252, 253, 254])
+def test_e8m0_scales_at_the_ends(xdt, T, byte):
+    """Weights up to 6 * 2^127, beyond float32 themselves: whole tokens times a
+    power of two bring the products back to whole numbers, which sum exactly.
+    A token that is zero under such weights takes nothing from them."""
+    rng = np.random.default_rng(byte)
+    m, n = 50, 700
+    codes = rng.integers(0, 16, size=(m, n)).astype(np.uint8)
+    sb = np.full((m, -(-n // 32)), byte, np.uint8)
+    c, s = fp4.store(codes, sb, MX)
+    k = rng.integers(-8, 9, size=(T, n)).astype(np.float64)
+    x = k * 2.0 ** min(max(127 - byte, -120), 120)   # tokens are normal numbers
+    y64 = x @ fp4.values(codes, sb, MX).T
+    y = matvec(dev(x.astype(np.float32)).to(xdt), (dev(c), dev(s), None), MX).view(torch.float32)
+    assert np.array_equal(y.double().cpu().numpy(), y64)
+    if T > 1:
+        x[1] = 0.0
+        y = matvec(dev(x.astype(np.float32)).to(xdt), (dev(c), dev(s), None), MX).view(torch.float32)
+        assert not y[1].any()
