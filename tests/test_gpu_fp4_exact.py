@@ -85,3 +85,54 @@ def test_e8m0_scales_at_the_ends(T, m, n):
     y = torch.empty(T, m, device=DEV)
     kq.kronq_fp4_matmul(dev(xq[0]), dev(xq[1]), dev(wq[0]), dev(wq[1]), MX, n, y)
     assert torch.equal(y.double(), want)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,m,n", [(1, 256, 40001), (100, 1000, 4095), (300, 300, 8191), (17, 520, 20033)])
+def test_split_columns(fmt, dt, T, m, n):
+    assert kq.kronq_fp4_matmul_workspace_bytes(T, m, n, fmt) > 0
+    rng = np.random.default_rng(n)
+    x, w = whole(rng, T, n, fmt), whole(rng, m, n, fmt)
+    y = torch.empty(T, m, dtype=dt, device=DEV)
+    kq.kronq_fp4_matmul(x[0], x[1], w[0], w[1], fmt, n, y, xg=x[2], wg=w[2])
+    assert torch.equal(y, product(x[3], w[3]).to(dt))
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes,m,n,pad", [([0, 200, 33, 0, 300, 1], 300, 4095, 3), ([64] * 9, 70, 545, 0), ([5, 7], 513, 28672, 2)])
+def test_groups(fmt, dt, sizes, m, n, pad):
+    rng = np.random.default_rng(n)
+    E, T = len(sizes), sum(sizes) + pad
+    x, w = whole(rng, T, n, fmt), whole(rng, E * m, n, fmt)
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    y = torch.full((T, m), 5.0, dtype=dt, device=DEV)
+    g = None if fmt == MX else 2.0 ** (torch.arange(E, device=DEV) % 3)
+    kq.kronq_fp4_grouped_matmul(x[0], x[1], dev(off), w[0].view(E, m, -1), w[1].view(E, m, -1), fmt, n, y, xg=x[2], wg=g)
+    want = torch.full((T, m), 5.0, dtype=torch.float64, device=DEV)
+    for e in range(E):
+        rows = slice(off[e], off[e + 1])
+        if off[e] < off[e + 1]:
+            want[rows] = product(x[3][rows], w[3][e * m:(e + 1) * m]) * (1.0 if g is None else float(g[e]))
+    assert torch.equal(y, want.to(dt))
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+@pytest.mark.parametrize("xdt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [1, 2, 8, 9, 16])
+@pytest.mark.parametrize("m,n", [(100, 28672), (33, 20001), (300, 1030), (5000, 130)])
+def test_few_tokens(fmt, xdt, T, m, n):
+    """Whole tokens: one in 64 has more bits than one fp16 part holds (float32), the others few."""
+    rng = np.random.default_rng(T + n)
+    w = whole(rng, m, n, fmt)
+    if n > 20000 and xdt is torch.float32 and T > 8:
+        assert kq.kronq_fp4_matvec_workspace_bytes(T, m, n, fmt) >= 16 * T * m * 4   # many slices
+    big = 4095 if xdt is torch.float32 else 127
+    k = np.where(rng.random((T, n)) < 1 / 64, rng.integers(-big, big + 1, size=(T, n)), rng.integers(-4, 5, size=(T, n)))
+    x = dev(k.astype(np.float32)).to(xdt)
+    # values of W are multiples of 2^-2: sums of these fit below 2^22
+    assert float((x.double().abs() @ w[3].abs().T).max()) < 2.0 ** 22
+    y = torch.empty(T, m, device=DEV)
+    kq.kronq_fp4_matvec(x, w[0], w[1], fmt, y, wg=w[2])
+    assert torch.equal(y.double(), x.double() @ w[3].T)
