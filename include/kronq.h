@@ -454,6 +454,9 @@ kronq_status kronq_decode_matvec(const uint32_t* packed, const float* scales, co
  *   KRONQ_NVFP4  blocks of 16, E4M3 scales (unsigned), and one positive
  *                float32 tensor scale in device memory:
  *                value = code * scale * gscale.
+ * The products multiply tokens and weights as they are: weights that
+ * kronq_biip_forward rotated go with tokens rotated alike, which none of these
+ * calls does, or are rotated back (kronq_biip_inverse) before they are quantised.
  * ------------------------------------------------------------------------- */
 typedef enum { KRONQ_MXFP4 = 0, KRONQ_NVFP4 = 1 } kronq_fp4_format;
 

@@ -22,12 +22,13 @@
 // the eight epilogue warps drain the accumulator into registers first and
 // release it before they store.
 //
-// Bound by the 1 kW power cap for long runs of large products (2048 x 28672 x
-// 8192 NVFP4 232 us, 4.2 PFLOP/s at 1.45 GHz; 8192 x 8192 x 28672 MXFP4 735 us, 5.2
-// PFLOP/s at 1.15 GHz, 0.85 and more of the tensor rate at that clock), by the
-// supply of operands and scales at full clocks, by HBM for few tokens (16 tokens,
-// 8192 x 28672 NVFP4 32 us, 0.62 of the measured rate with the columns split),
-// by latency below that (100 x 1000 x 4095 9 us in four parts).
+// Bound by the 1 kW power cap for long runs of large products (back to back for
+// seconds 2048 x 28672 x 8192 NVFP4 246 us, 3.9 PFLOP/s at 1.48 GHz, and 8192 x 8192
+// x 28672 MXFP4 779 us, 4.9 PFLOP/s at 1.24 GHz, 0.82 of the tensor rate at that
+// clock; 209 and 723 us before the clock falls), by the supply of operands and
+// scales at full clocks, by HBM for few tokens (16 tokens, 8192 x 28672 NVFP4
+// 32 us, 0.62 of the measured rate with the columns split), by latency below that
+// (100 x 1000 x 4095 9 us in four parts).
 //
 // The loaders of both CTAs arrive at the even CTA's barrier, whose MMA thread
 // copies the scales of both.  Each loader's stores go behind a proxy fence (the

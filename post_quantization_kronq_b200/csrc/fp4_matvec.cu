@@ -14,21 +14,25 @@
 // on the N side: one weight load serves 8 tokens at the price of one.
 //
 // Measured: 28672 x 8192 NVFP4 with one bf16 token 38 us (0.53 of the measured
-// HBM rate), eight 52 us; 8192 x 28672 MXFP4 with five float32 tokens 58 us;
-// 4096 x 4096 NVFP4 with one 7.5 us.  Above a stream of the weights alone
-// (29 us) it is bound by its instructions, 175 a warp and span.
+// HBM rate), eight 52 us, 16 float32 ones 108 us; 8192 x 28672 MXFP4 with five
+// float32 tokens 58 us; 4096 x 4096 NVFP4 with one 7.3 us.  Above a stream of the
+// weights alone (29 us) it is bound by its instructions, 172 a warp and span.
 //
 // Both operands are exact in fp16, or nearly so.  A weight is E2M1 times its
 // block scale, at most 6 significant bits: one conversion and one
 // multiplication for two weights (E8M0 scales are taken times 2^12, good for
 // 2^-35 .. 2^1).  A token's span of 128 columns is scaled by a power of two
 // that brings its largest magnitude to [2^14, 2^15): bf16 values down to
-// 2^-31 of it are exact; a float32 value is two parts of 11 bits (2^-23 off
-// at most) down to 2^-28 of it.  The sum over a span is scaled back when it
+// 2^-31 of it are exact; a float32 value down to 2^-28 of it is two parts of 11
+// bits (2^-23 off at most; 2^-22 in the lowest binade, where the second is
+// subnormal: a third part would cost half as much again).  The sum over a span is scaled back when it
 // joins the float32 sum of the row.  What this does not cover is computed in
 // float32, one weight and token at a time: a token's span with a wider range
 // within its 128 columns, infinities or NaN, and a block whose E8M0 scale is
-// beyond the range.  The mma sees zeros there, so that neither the other tokens
+// beyond the range, unless it holds zeros alone (the quantiser's own scale for
+// those is the lowest).  28672 x 8192: a bf16 token whose spans are all wide 140 us
+// alone and 214 us among five; one MXFP4 block of zeros in a hundred 45 us
+// against 40.  The mma sees zeros there, so that neither the other tokens
 // of a call nor the other rows of a tile are summed in another order.
 //
 // The order of k inside an mma is free as long as weights and tokens agree:
