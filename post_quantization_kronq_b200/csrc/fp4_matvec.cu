@@ -25,15 +25,15 @@
 // that brings its largest magnitude to [2^14, 2^15): bf16 values down to
 // 2^-31 of it are exact; a float32 value down to 2^-28 of it is two parts of 11
 // bits (2^-23 off at most; 2^-22 in the lowest binade, where the second is
-// subnormal: a third part would cost half as much again).  The sum over a span is scaled back when it
-// joins the float32 sum of the row.  What this does not cover is computed in
-// float32, one weight and token at a time: a token's span with a wider range
-// within its 128 columns, infinities or NaN, and a block whose E8M0 scale is
-// beyond the range, unless it holds zeros alone (the quantiser's own scale for
-// those is the lowest).  28672 x 8192: a bf16 token whose spans are all wide 140 us
-// alone and 214 us among five; one MXFP4 block of zeros in a hundred 45 us
-// against 40.  The mma sees zeros there, so that neither the other tokens
-// of a call nor the other rows of a tile are summed in another order.
+// subnormal: a third part would cost half as much again).  The sum over a span
+// is scaled back when it joins the float32 sum of the row.  What this does not
+// cover is computed in float32, one weight and token at a time: a token's span
+// with a wider range within its 128 columns, infinities or NaN, and a block whose
+// E8M0 scale is beyond the range, unless it holds zeros alone (the quantiser's own
+// scale for those is the lowest).  The mma sees zeros there, so that neither the
+// other tokens of a call nor the other rows of a tile are summed in another order.
+// 28672 x 8192: a bf16 token whose spans are all wide 140 us alone and 214 us among
+// five; one MXFP4 block of zeros in a hundred 45 us against 40.
 //
 // The order of k inside an mma is free as long as weights and tokens agree:
 // lane t of a span holds k = 32 t + 8 j + {0..7} as word j.  Tokens are staged
@@ -104,8 +104,9 @@ template <int FMT, bool XF32, int NT>
 struct Vec {
   static constexpr int PARTS = XF32 ? 2 : 1;
   static constexpr int BPL = FMT == KRONQ_NVFP4 ? 2 : 1;   // scale blocks of a lane's 32 columns
-  // spans of a step that are multiplied together, so that four chains of mma
-  // are in flight and the registers suffice
+  // spans of a step that are multiplied together, so that four chains of mma are
+  // in flight and the registers suffice (16 float32 tokens, 28672 x 8192 MXFP4: 142 us
+  // with both spans together, 131 with one; NVFP4 109 and 111)
   static constexpr int AT_ONCE = NT * PARTS >= 4 ? 1 : PAIR;
 
   struct Load {
@@ -219,8 +220,8 @@ struct Vec {
   static __device__ __forceinline__ void step(const VecArgs& a, const uint8_t* slot, int left, const uint8_t* const (&xs)[NT], int xnext, const float* fac, int fnext,
                                               uint32_t apart0, uint32_t apart1, int64_t kend, int lane, float (&acc)[NT][4]) {
     bool odd = false;
-    // no token left for the mma (looked at for few tokens, where it is likely: one token whose spans are all
-    // wide 166 -> 142 us, but 16 float32 tokens that are not 119 -> 125)
+    // no token left for the mma (looked at for few tokens, where it is likely: one
+    // token whose spans are all wide 166 -> 142 us, but 16 float32 ones 119 -> 125)
     const bool none = NT == 1 && (apart0 & apart1) == (1u << a.T) - 1u;
 #pragma unroll
     for (int s0 = 0; s0 < PAIR && !none; s0 += AT_ONCE) {
